@@ -103,11 +103,19 @@ typedef struct flint_moe_weights {
 /* Device-side check codes recorded in the workspace status word. */
 enum {
   FLINT_DEVCHECK_EXPERT_ID = 1,   /* an expert id outside [0, E) reached a kernel */
-  FLINT_DEVCHECK_NONFINITE = 2,   /* a non-finite weight reached the packer */
+  FLINT_DEVCHECK_NONFINITE = 2,   /* a non-finite weight reached the packer; a row of
+                                     logits with nothing to sample */
   FLINT_DEVCHECK_WAIT = 4,        /* a bounded wait gave up (FLINT_ERR_TIMEOUT) */
   FLINT_DEVCHECK_MMA = 8,         /* the tensor-core path rejected a tile */
-  FLINT_DEVCHECK_INDEX = 16       /* a position or cache slot outside its range (skipped) */
+  FLINT_DEVCHECK_INDEX = 16       /* a position, cache slot, page, length or sampling
+                                     parameter outside its range (skipped) */
 };
+
+/* Element type of a paged KV cache. E4M3 caches hold value / scale, one fp32
+ * scale per kv head for keys and one for values. */
+typedef enum flint_kv_dtype { FLINT_KV_BF16 = 0, FLINT_KV_E4M3 = 1 } flint_kv_dtype;
+
+typedef enum flint_logits_dtype { FLINT_LOGITS_F32 = 0, FLINT_LOGITS_BF16 = 1 } flint_logits_dtype;
 
 typedef enum flint_path {
   FLINT_PATH_AUTO = 0, /* NVFP4: GEMV kernels below 32 tokens, tensor-core path from
@@ -428,6 +436,114 @@ int flint_decode_attention(const uint16_t* q, const uint16_t* k_cache, const uin
                            const int64_t* start, const int32_t* len, int32_t T, int32_t n_q_heads,
                            int32_t n_kv_heads, int32_t head_dim, int32_t max_len, float scale, uint16_t* out,
                            void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* ---- Paged KV cache -------------------------------------------------------
+ * The three calls below are the serving step of a batch of sequences around the
+ * layer: append the new tokens' keys and values, attend, and (after the output
+ * head) sample. Common arguments:
+ *   q_start   device int32 [B + 1]: sequence s owns the token rows q_start[s]
+ *             .. q_start[s+1] - 1 (non-decreasing; n_s of them, 0 allowed).
+ *             Rows outside [q_start[0], q_start[B]) belong to no sequence:
+ *             nothing of theirs is written.
+ *   kv_len    device int32 [B]: cached positions of the sequence INCLUDING its
+ *             n_s new tokens, which are its last ones: new token i sits at
+ *             position kv_len[s] - n_s + i.
+ *   block_table  device int32 [B][max_pages]: position p lives in page
+ *             block_table[s][p / page_size], row p % page_size. Entries past
+ *             the last used page are not read.
+ *   k_cache, v_cache  device pools [n_pages][page_size][n_kv_heads][128] of
+ *             cache_dtype (flint_kv_dtype); page_size a power of two in
+ *             16..1024, n_pages * page_size < 2^31.
+ *   k_scale, v_scale  device fp32 [n_kv_heads] for an E4M3 cache (a stored code
+ *             stands for code * scale); ignored (NULL allowed) for bf16.
+ *   status    nullable device int32: FLINT_DEVCHECK_INDEX is set by a page
+ *             outside [0, n_pages), a kv_len[s] below n_s or above max_pages *
+ *             page_size, or token rows outside [0, T).
+ * All of it is read on the device only, so a captured graph replays with other
+ * lengths and pages. head_dim must be 128. Pointers of vectors 16-byte aligned,
+ * others 4-byte. The pages of the sources fix none of this: the paged layout
+ * and its block table are the usual serving form of the cache. */
+
+/* flint_qk_norm_rope_paged_kv -- flint_qk_norm_rope_kv on a paged cache:
+ * normalise and rotate the new tokens' queries and keys, write q_out and append
+ * keys and values to their pages.
+ *   qkv      device bf16 [T][n_q_heads + 2*n_kv_heads][128]
+ *   q_norm_w, k_norm_w  device bf16 [128], or both NULL: no normalisation
+ *   cos_sin, max_pos, rope  as there; the row is the token's position
+ *   q_out    device bf16 [T][n_q_heads][128]
+ * One rounding, from fp32: to bf16, or for an E4M3 cache of y / scale to the
+ * nearest code, saturating at +-448. A token without a valid page keeps its
+ * key and value unwritten, one whose position is at or past max_pos its
+ * rotation undone (its page is written); both set FLINT_DEVCHECK_INDEX. Two
+ * tokens never share a cache row unless the block table maps them there (then
+ * either may win). One kernel, asynchronous on `stream`. */
+int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32_t n_q_heads, int32_t n_kv_heads,
+                                int32_t head_dim, const uint16_t* q_norm_w, const uint16_t* k_norm_w,
+                                const float* cos_sin, int32_t max_pos, int32_t rope, float eps,
+                                const int32_t* q_start, const int32_t* kv_len, int32_t B,
+                                const int32_t* block_table, int32_t max_pages, int32_t page_size, int64_t n_pages,
+                                int32_t cache_dtype, const float* k_scale, const float* v_scale, uint16_t* q_out,
+                                void* k_cache, void* v_cache, int32_t* status, void* stream);
+
+/* flint_paged_attention -- attention of each sequence's new tokens over its
+ * cache (the new tokens' own keys and values already appended):
+ *   out[t][h] = sum_j w_j v_j,  w = softmax_j(scale * q[t][h] . k_j)
+ * over the positions j of the sequence with pos - window < j <= pos, pos the
+ * token's position (window 0: every j <= pos), keys and values of kv head h /
+ * (n_q_heads / n_kv_heads). fp32 scores, maxima and sums; the weights enter the
+ * value sum rounded to bf16 (bf16 cache) or f16 (E4M3 cache, whose codes are
+ * exact in f16; q then enters as f16 after an exact power-of-two scale per row).
+ * A sequence with an invalid kv_len, or with more than max_q_len new tokens,
+ * gives zeros (FLINT_DEVCHECK_INDEX); the keys and values of an invalid page
+ * count as zero vectors. Keys and values inside a sequence's length have to be
+ * finite: one that is not may reach every query of its sequence. Unwritten
+ * rows and other sequences' rows may hold anything.
+ *   q, out    device bf16 [T][n_q_heads][128]; out must not overlap the inputs
+ *   max_q_len host upper bound of n_s. max_q_len * (n_q_heads / n_kv_heads) <=
+ *             16 takes the decode kernel (register-fragment tensor cores, keys
+ *             split evenly over the GPU), more the chunk kernel (tcgen05).
+ *   workspace flint_paged_attention_workspace_bytes(T, B, n_q_heads, n_kv_heads,
+ *             max_q_len) bytes, 16-byte aligned, overwritten by every call; calls
+ *             that may run at the same time need one each.
+ * n_q_heads / n_kv_heads an integer <= 16, n_q_heads <= 1024, B <= 65535,
+ * T <= 2^24, window >= 0, scale finite and > 0. Asynchronous on `stream`. */
+size_t flint_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t n_q_heads, int32_t n_kv_heads,
+                                             int32_t max_q_len);
+int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t* q_start, const int32_t* kv_len, int32_t B,
+                          const int32_t* block_table, int32_t max_pages, int32_t page_size, int64_t n_pages,
+                          const void* k_cache, const void* v_cache, int32_t cache_dtype, const float* k_scale,
+                          const float* v_scale, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                          int32_t max_q_len, int32_t window, float scale, uint16_t* out, void* workspace,
+                          size_t workspace_bytes, int32_t* status, void* stream);
+
+/* flint_sample -- one token per row of logits, from given uniform numbers.
+ *   logits      device, element type logits_dtype (flint_logits_dtype), row r
+ *               at logits + r * row_stride elements (row_stride >= vocab). NaN
+ *               counts as -inf.
+ *   temperature device fp32 [rows] or NULL (1). 0: the largest logit (lowest
+ *               index of equals), log-probability 0.
+ *   top_k       device int32 [rows] or NULL; <= 0 or >= vocab: no limit
+ *   top_p       device fp32 [rows] or NULL; >= 1: no limit
+ *   min_p       device fp32 [rows] or NULL; <= 0: no limit
+ *   u           device fp32 [rows], in [0, 1)
+ *   tokens      device int32 [rows]; logprobs device fp32 [rows] or NULL
+ * With w_i = exp((x_i - max x) / temperature) and the order "larger logit, then
+ * lower index": keep the first top_k tokens; of those, each whose predecessors
+ * hold less than top_p of their summed w (the first one always); of those, each
+ * with w_i >= min_p (the largest always). The token is the first index, in
+ * vocabulary order, whose running sum of kept w exceeds u times the kept total;
+ * its log-probability is ln(w / kept total). Masses are summed as integers of
+ * 2^-44 of the largest (coarser above 2^18 tokens): the result is the same in
+ * every run, and a token below half of that is never drawn.
+ *   status      nullable device int32. A row without any logit above -inf sets
+ *               FLINT_DEVCHECK_NONFINITE, one with a negative or NaN temperature
+ *               or u outside [0, 1) FLINT_DEVCHECK_INDEX; both give token -1,
+ *               log-probability -inf.
+ * vocab, rows <= 2^24. One kernel (a thread-block cluster per row), no
+ * workspace, asynchronous on `stream`. */
+int flint_sample(const void* logits, int32_t rows, int32_t vocab, int64_t row_stride, int32_t logits_dtype,
+                 const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                 const float* u, int32_t* tokens, float* logprobs, int32_t* status, void* stream);
 
 /* Synchronises `stream`, reads the workspace status word into *device_flags
  * (FLINT_DEVCHECK_* bits, may be NULL) and clears it. Returns FLINT_OK, or

@@ -25,6 +25,8 @@ __all__ = [
     "flint_debug_dequant", "flint_debug_decode", "flint_debug_group", "flint_debug_wait_timeout", "flint_version",
     "flint_qk_norm_rope_kv", "flint_decode_attention", "flint_decode_attention_workspace_bytes",
     "flint_moe_forward_routed", "flint_ep_dispatch", "flint_ep_combine",
+    "FLINT_KV_BF16", "FLINT_KV_E4M3", "FLINT_LOGITS_F32", "FLINT_LOGITS_BF16",
+    "flint_qk_norm_rope_paged_kv", "flint_paged_attention", "flint_paged_attention_workspace_bytes", "flint_sample",
 ]
 
 FLINT_W_NVFP4, FLINT_W_BF16 = 0, 1
@@ -32,6 +34,8 @@ FLINT_PATH_AUTO, FLINT_PATH_GEMV, FLINT_PATH_MMA = 0, 1, 2
 FLINT_LAYER_AUTO, FLINT_LAYER_FMA, FLINT_LAYER_MMA, FLINT_LAYER_CLUSTER = 0, 1, 2, 3
 FLINT_DEVCHECK_EXPERT_ID, FLINT_DEVCHECK_NONFINITE, FLINT_DEVCHECK_WAIT, FLINT_DEVCHECK_MMA = 1, 2, 4, 8
 FLINT_DEVCHECK_INDEX = 16
+FLINT_KV_BF16, FLINT_KV_E4M3 = 0, 1
+FLINT_LOGITS_F32, FLINT_LOGITS_BF16 = 0, 1
 FLINT_ERR_DEVICE_CHECK, FLINT_ERR_TIMEOUT = -6, -7
 STATUS_NAMES = {0: "FLINT_OK", -1: "FLINT_ERR_INVALID_ARG", -2: "FLINT_ERR_UNSUPPORTED_SHAPE",
                 -3: "FLINT_ERR_MISALIGNED", -4: "FLINT_ERR_WORKSPACE", -5: "FLINT_ERR_CUDA",
@@ -117,6 +121,17 @@ def lib() -> ctypes.CDLL:
         L.flint_ep_dispatch.restype = i32
         L.flint_ep_combine.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp]
         L.flint_ep_combine.restype = i32
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        L.flint_qk_norm_rope_paged_kv.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, i32, i32, f32, vp, vp, i32, vp,
+                                                  i32, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp]
+        L.flint_qk_norm_rope_paged_kv.restype = i32
+        L.flint_paged_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.flint_paged_attention_workspace_bytes.restype = sz
+        L.flint_paged_attention.argtypes = [vp, i32, vp, vp, i32, vp, i32, i32, i64, vp, vp, i32, vp, vp, i32, i32,
+                                            i32, i32, i32, f32, vp, vp, sz, vp, vp]
+        L.flint_paged_attention.restype = i32
+        L.flint_sample.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.flint_sample.restype = i32
         L.flint_moe_workspace_init.argtypes = [vp, sz, vp]
         L.flint_moe_workspace_init.restype = i32
         L.flint_moe_get_status.argtypes = [vp, P(i32), vp]
@@ -164,6 +179,24 @@ def _check(rc: int):
 
 def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
+
+
+def _checked(**tensors):
+    """Refuses tensors that the kernels would read wrongly: strided ones, and
+    ones on another device than the current one (whose stream the call takes).
+    Each is (tensor, bytes the call reads or writes)."""
+    import torch
+    for name, (t, need) in tensors.items():
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda:
+            raise FlintError(-1, f"{name}: expected a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise FlintError(-1, f"{name}: on {t.device}, the current device is {torch.cuda.current_device()}")
+        if not t.is_contiguous():
+            raise FlintError(-1, f"{name}: not contiguous")
+        if _nbytes(t) < need:
+            raise FlintError(-1, f"{name}: {_nbytes(t)} bytes, {need} needed")
 
 
 def flint_last_error() -> str:
@@ -303,6 +336,69 @@ def flint_ep_dispatch(topk_ids, topk_weights, T: int, top_k: int, n_shared: int,
 def flint_ep_combine(y, pair_pos, T: int, slots: int, d: int, residual, out, stream=None) -> None:
     _check(lib().flint_ep_combine(_ptr(y), _ptr(pair_pos), int(T), int(slots), int(d), _ptr(residual), _ptr(out),
                                   _stream(stream)))
+
+
+def _check_paged(T, n_q_heads, n_kv_heads, q_start, kv_len, B, block_table, max_pages, page_size, n_pages, cache_dtype,
+                 k_scale, v_scale, k_cache, v_cache, status, head_dim):
+    T, B, mp = max(int(T), 0), max(int(B), 0), max(int(max_pages), 0)
+    pool = max(int(n_pages), 0) * max(int(page_size), 0) * int(n_kv_heads) * int(head_dim) * (
+        1 if cache_dtype == FLINT_KV_E4M3 else 2)
+    scales = 4 * int(n_kv_heads) if cache_dtype == FLINT_KV_E4M3 else 0
+    live = T > 0 and B > 0
+    _checked(q_start=(q_start, 4 * (B + 1) * live), kv_len=(kv_len, 4 * B * live),
+             block_table=(block_table, 4 * B * mp * live), k_cache=(k_cache, pool), v_cache=(v_cache, pool),
+             k_scale=(k_scale, scales), v_scale=(v_scale, scales), status=(status, 4))
+
+
+def flint_qk_norm_rope_paged_kv(qkv, T: int, n_q_heads: int, n_kv_heads: int, q_norm_w, k_norm_w, cos_sin,
+                                max_pos: int, rope: bool, eps: float, q_start, kv_len, B: int, block_table,
+                                max_pages: int, page_size: int, n_pages: int, cache_dtype: int, k_scale, v_scale,
+                                q_out, k_cache, v_cache, status=None, head_dim: int = 128, stream=None) -> None:
+    _check_paged(T, n_q_heads, n_kv_heads, q_start, kv_len, B, block_table, max_pages, page_size, n_pages, cache_dtype,
+                 k_scale, v_scale, k_cache, v_cache, status, head_dim)
+    row = 2 * max(int(T), 0) * int(head_dim)
+    _checked(qkv=(qkv, row * (n_q_heads + 2 * n_kv_heads)), q_out=(q_out, row * n_q_heads),
+             q_norm_w=(q_norm_w, 2 * head_dim), k_norm_w=(k_norm_w, 2 * head_dim),
+             cos_sin=(cos_sin, 4 * head_dim * max(int(max_pos), 0) if rope else 0))
+    _check(lib().flint_qk_norm_rope_paged_kv(
+        _ptr(qkv), int(T), int(n_q_heads), int(n_kv_heads), int(head_dim), _ptr(q_norm_w), _ptr(k_norm_w),
+        _ptr(cos_sin), int(max_pos), int(bool(rope)), float(eps), _ptr(q_start), _ptr(kv_len), int(B),
+        _ptr(block_table), int(max_pages), int(page_size), int(n_pages), int(cache_dtype), _ptr(k_scale),
+        _ptr(v_scale), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(status), _stream(stream)))
+
+
+def flint_paged_attention_workspace_bytes(T: int, B: int, n_q_heads: int, n_kv_heads: int, max_q_len: int) -> int:
+    return int(lib().flint_paged_attention_workspace_bytes(int(T), int(B), int(n_q_heads), int(n_kv_heads),
+                                                           int(max_q_len)))
+
+
+def flint_paged_attention(q, T: int, q_start, kv_len, B: int, block_table, max_pages: int, page_size: int,
+                          n_pages: int, k_cache, v_cache, cache_dtype: int, k_scale, v_scale, n_q_heads: int,
+                          n_kv_heads: int, max_q_len: int, window: int, scale: float, out, workspace, status=None,
+                          head_dim: int = 128, stream=None) -> None:
+    _check_paged(T, n_q_heads, n_kv_heads, q_start, kv_len, B, block_table, max_pages, page_size, n_pages, cache_dtype,
+                 k_scale, v_scale, k_cache, v_cache, status, head_dim)
+    row = 2 * max(int(T), 0) * int(head_dim) * int(n_q_heads)
+    _checked(q=(q, row), out=(out, row), workspace=(workspace, 0))
+    _check(lib().flint_paged_attention(
+        _ptr(q), int(T), _ptr(q_start), _ptr(kv_len), int(B), _ptr(block_table), int(max_pages), int(page_size),
+        int(n_pages), _ptr(k_cache), _ptr(v_cache), int(cache_dtype), _ptr(k_scale), _ptr(v_scale), int(n_q_heads),
+        int(n_kv_heads), int(head_dim), int(max_q_len), int(window), float(scale), _ptr(out), _ptr(workspace),
+        _nbytes(workspace), _ptr(status), _stream(stream)))
+
+
+def flint_sample(logits, rows: int, vocab: int, row_stride: int, logits_dtype: int, temperature, top_k, top_p, min_p,
+                 u, tokens, logprobs=None, status=None, stream=None) -> None:
+    r = max(int(rows), 0)
+    per_row = 4 * r
+    es = 4 if logits_dtype == FLINT_LOGITS_F32 else 2
+    _checked(logits=(logits, es * ((r - 1) * int(row_stride) + int(vocab)) if r else 0),
+             temperature=(temperature, per_row), top_k=(top_k, per_row), top_p=(top_p, per_row),
+             min_p=(min_p, per_row), u=(u, per_row), tokens=(tokens, per_row), logprobs=(logprobs, per_row),
+             status=(status, 4))
+    _check(lib().flint_sample(_ptr(logits), int(rows), int(vocab), int(row_stride), int(logits_dtype),
+                              _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(tokens),
+                              _ptr(logprobs), _ptr(status), _stream(stream)))
 
 
 def flint_moe_get_status(workspace, stream=None) -> tuple[int, int]:

@@ -1,0 +1,136 @@
+"""Attention of new tokens over the paged cache against its 64-bit form: decode and chunk calls, both cache types, head
+layouts, page sizes, ragged and empty sequences, windows, rows of no sequence, lengths and pages that are invalid.
+Everything the sequences do not own holds NaN. Bounds: paged_ref.check_attention."""
+import pytest
+import torch
+
+import nvfp4_weight_only_flint_b200 as fm
+import paged_ref as R
+
+pytestmark = pytest.mark.gpu
+
+DECODE = [([1], [1]), ([1], [17]), ([1], [4097]), ([1, 1, 1], [64, 65, 1000]), ([2, 1, 0, 2], [2, 300, 40, 129]),
+          ([1] * 70, [3 + 29 * i for i in range(70)])]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("case", range(len(DECODE)))
+def test_decode_lengths(case, e4m3):
+    new, kv = DECODE[case]
+    b = R.Paged(100 + case, new, kv, 32, 4, 16, e4m3)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    R.check_attention(R.run_attention(b, status=st), b, what=str((new[:4], kv[:4])))
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv,page", [(1, 1, 16), (3, 3, 32), (14, 2, 64), (16, 1, 128), (12, 4, 1024), (26, 2, 16)])
+def test_decode_head_layouts(hq, hkv, page, e4m3):
+    b = R.Paged(hq + page, [1, 1, 1], [5, 700, 130], hq, hkv, page, e4m3)
+    R.check_attention(R.run_attention(b), b, what=f"{hq}/{hkv}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window", [1, 15, 64, 700])
+def test_decode_window(window, e4m3):
+    b = R.Paged(window, [2, 1, 2], [2, 900, 333], 16, 2, 16, e4m3)
+    R.check_attention(R.run_attention(b, window), b, window, what=f"window {window}")
+
+
+def test_decode_peaked_scores():
+    b = R.Paged(50, [1, 1], [3000, 200], q_gain=5.0)
+    R.check_attention(R.run_attention(b), b, what="peaked")
+    b = R.Paged(51, [1, 1], [3000, 200], q_gain=5.0, e4m3=True)
+    R.check_attention(R.run_attention(b), b, what="peaked, e4m3")
+
+
+def _invalid(new, kv, e4m3, hq=8, hkv=2):
+    """What invalid lengths, rows and pages give, for a decode or a chunk call."""
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mq = max(new)
+    b = R.Paged(60, new, kv, hq, hkv, 16, e4m3, pad=2)
+    got = R.run_attention(b, status=st, max_q=mq)
+    assert int(st.item()) == 0
+    R.check_attention(got, b)
+    assert got[b.rows:].isnan().all()  # rows of no sequence keep the sentinel
+    # a length below its new tokens, or past the block table: zeros, the others as before
+    for bad in (new[1] - 1, -5, 16 * b.max_pages + 1, 2 ** 31 - 1):
+        b = R.Paged(60, new, kv, hq, hkv, 16, e4m3, pad=2)
+        b.kv_len[1] = bad
+        st.zero_()
+        out = R.run_attention(b, status=st, max_q=mq)
+        assert int(st.item()) == fm.FLINT_DEVCHECK_INDEX
+        r = slice(int(b.q_start[1]), int(b.q_start[2]))
+        assert (out[r] == 0).all()
+        out[r] = got[r]
+        R.check_attention(out, b)
+    # a page outside the pool counts as zero keys and values
+    b = R.Paged(60, new, kv, hq, hkv, 16, e4m3, pad=2)
+    b.table[2, 1], b.table[2, 3] = -1, b.n_pages
+    st.zero_()
+    out = R.run_attention(b, status=st, max_q=mq)
+    assert int(st.item()) == fm.FLINT_DEVCHECK_INDEX
+    R.check_attention(out, b)
+    # token rows outside the call
+    b = R.Paged(60, new, kv, hq, hkv, 16, e4m3, pad=2)
+    b.q_start[-1] = b.T + 1
+    st.zero_()
+    out = R.run_attention(b, status=st, max_q=mq)
+    assert int(st.item()) == fm.FLINT_DEVCHECK_INDEX
+    last = slice(int(b.q_start[-2]), b.T)
+    assert out[last].isnan().all()
+    out[last] = got[last]
+    R.check_attention(out, b)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_invalid(e4m3):
+    _invalid([1, 2, 1, 2], [20, 50, 100, 33], e4m3)
+
+
+def test_decode_more_tokens_than_announced():
+    b = R.Paged(70, [1, 3, 1], [30, 30, 30], 8, 2, 16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = R.run_attention(b, status=st, max_q=2)
+    assert int(st.item()) == fm.FLINT_DEVCHECK_INDEX
+    assert (out[1:4] == 0).all()
+    out[1:4] = R.attention(b)[1:4]
+    R.check_attention(out, b)
+
+
+def test_decode_split_is_the_same_in_every_run_and_graph():
+    b = R.Paged(80, [1] * 5, [9000, 17, 4000, 1, 2500])
+    c = b.cuda
+    dev = [c(x) for x in (b.q, b.q_start, b.kv_len, b.table, b.k, b.v)]
+    ws = torch.empty(fm.flint_paged_attention_workspace_bytes(b.T, b.B, 32, 4, 1), dtype=torch.uint8, device="cuda")
+    out = torch.empty((b.T, 32, R.DH), dtype=torch.bfloat16, device="cuda")
+
+    def call(o=out, w=ws, stream=None):
+        fm.flint_paged_attention(dev[0], b.T, dev[1], dev[2], b.B, dev[3], b.max_pages, 16, b.n_pages, dev[4], dev[5],
+                                 fm.FLINT_KV_BF16, None, None, 32, 4, 1, 0, R.DH ** -0.5, o, w, stream=stream)
+    call()
+    torch.cuda.synchronize()
+    first = out.clone()
+    R.check_attention(first.cpu().double(), b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    # the same graph with other lengths
+    b.kv = [3000, 17, 1, 1, 2400]
+    dev[2].copy_(torch.tensor(b.kv, dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    R.check_attention(out.cpu().double(), b)
+    # two calls at once, each with its own workspace
+    side = torch.cuda.Stream()
+    o2, w2 = torch.empty_like(out), torch.empty_like(ws)
+    side.wait_stream(torch.cuda.current_stream())
+    call()
+    call(o2, w2, side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, o2)

@@ -1,0 +1,107 @@
+"""Host-side checks of the paged serving operators: bad arguments are refused before anything is launched, and empty
+calls are no-ops (no GPU needed: the pointers below are never dereferenced)."""
+import pytest
+
+import nvfp4_weight_only_flint_b200 as fm
+from nvfp4_weight_only_flint_b200 import build as fbuild
+
+A = 0x100000
+
+
+@pytest.fixture(scope="module")
+def L():
+    fbuild.build()
+    return fm.lib()
+
+
+BATCH = dict(T=4, B=2, mp=8, page=16, pages=64, dt=0, ks=None, vs=None, qs=A, kl=A, bt=A, k=A, v=A, dh=128, hq=32,
+             hkv=4)
+BAD_BATCH = [(dict(page=8), -2), (dict(page=24), -2), (dict(page=2048), -2), (dict(dt=2), -1), (dict(T=-1), -1),
+             (dict(B=-1), -1), (dict(mp=-1), -1), (dict(pages=-1), -1), (dict(pages=1 << 27), -2), (dict(qs=None), -1),
+             (dict(kl=None), -1), (dict(bt=None), -1), (dict(k=None), -1), (dict(v=None), -1), (dict(dt=1), -1),
+             (dict(dt=1, ks=A), -1), (dict(k=A + 8), -3), (dict(v=A + 2), -3), (dict(qs=A + 2), -3),
+             (dict(dt=1, ks=A, vs=A + 1), -3), (dict(dh=64), -2), (dict(hq=0), -1), (dict(hkv=0), -1)]
+
+
+def _append(L, qkv=A, qw=A, kw=A, cs=A, max_pos=16, rope=1, eps=1e-6, q_out=A, **kw2):
+    b = {**BATCH, **kw2}
+    return L.flint_qk_norm_rope_paged_kv(qkv, b["T"], b["hq"], b["hkv"], b["dh"], qw, kw, cs, max_pos, rope, eps,
+                                         b["qs"], b["kl"], b["B"], b["bt"], b["mp"], b["page"], b["pages"], b["dt"],
+                                         b["ks"], b["vs"], q_out, b["k"], b["v"], None, None)
+
+
+def _attn(L, q=A, out=A, max_q=1, window=0, scale=0.088, ws=A, ws_bytes=1 << 40, **kw2):
+    b = {**BATCH, **kw2}
+    return L.flint_paged_attention(q, b["T"], b["qs"], b["kl"], b["B"], b["bt"], b["mp"], b["page"], b["pages"],
+                                   b["k"], b["v"], b["dt"], b["ks"], b["vs"], b["hq"], b["hkv"], b["dh"], max_q,
+                                   window, scale, out, ws, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("bad,rc", BAD_BATCH)
+def test_batch_arguments(L, bad, rc):
+    assert _append(L, **bad) == rc
+    assert _attn(L, **bad) == rc
+    assert fm.flint_last_error()
+
+
+def test_append_arguments(L):
+    assert _append(L, qkv=None) == -1
+    assert _append(L, q_out=None) == -1
+    assert _append(L, qw=None) == -1          # one weight without the other
+    assert _append(L, cs=None) == -1
+    assert _append(L, max_pos=0) == -1
+    assert _append(L, eps=-1.0) == -1
+    assert _append(L, eps=float("nan")) == -1
+    assert _append(L, qkv=A + 8) == -3
+    assert _append(L, cs=A + 4) == -3
+    assert _append(L, T=0) == 0
+    assert _append(L, B=0) == 0
+
+
+def test_attention_arguments(L):
+    assert _attn(L, q=None) == -1
+    assert _attn(L, out=None) == -1
+    assert _attn(L, q=A + 8) == -3
+    assert _attn(L, ws=A + 8) == -3
+    assert _attn(L, hq=34, hkv=2) == -2       # 17 query heads per kv head
+    assert _attn(L, hq=30) == -2
+    assert _attn(L, hq=2048, hkv=128) == -2
+    assert _attn(L, B=65536) == -2
+    assert _attn(L, max_q=0) == -1
+    assert _attn(L, window=-1) == -1
+    for s in (0.0, -1.0, float("nan"), float("inf")):
+        assert _attn(L, scale=s) == -1
+    assert _attn(L, T=0) == 0
+    assert _attn(L, B=0) == 0
+    for mq in (1, 2):
+        need = fm.flint_paged_attention_workspace_bytes(4, 2, 32, 4, mq)
+        assert need > 0
+        assert _attn(L, max_q=mq, ws_bytes=need - 1) == -4
+        assert _attn(L, max_q=mq, ws=None) == -4
+    for bad in ((0, 2, 32, 4, 1), (4, 0, 32, 4, 1), (4, 2, 30, 4, 1), (4, 2, 34, 2, 1), (4, 2, 32, 4, 0)):
+        assert fm.flint_paged_attention_workspace_bytes(*bad) == 0
+
+
+def _sample(L, logits=A, rows=2, vocab=100, stride=100, dt=0, t=A, k=A, p=A, m=A, u=A, tok=A, lp=A):
+    return L.flint_sample(logits, rows, vocab, stride, dt, t, k, p, m, u, tok, lp, None, None)
+
+
+def test_sample_arguments(L):
+    assert _sample(L, dt=2) == -1
+    assert _sample(L, rows=-1) == -1
+    assert _sample(L, vocab=0) == -1
+    assert _sample(L, stride=99) == -1
+    assert _sample(L, vocab=(1 << 24) + 1, stride=1 << 25) == -2
+    for name in ("logits", "u", "tok"):
+        assert _sample(L, **{name: None}) == -1
+    for name in ("logits", "t", "k", "p", "m", "u", "tok", "lp"):
+        assert _sample(L, **{name: A + 2}) == -3
+    assert _sample(L, logits=A + 1, dt=1) == -3
+    assert _sample(L, rows=0) == 0
+
+
+def test_python_wrappers_refuse_cpu_tensors():
+    import torch
+    x = torch.zeros(1000)
+    with pytest.raises(fm.FlintError):
+        fm.flint_sample(x, 1, 100, 100, fm.FLINT_LOGITS_F32, None, None, None, None, x, x)
