@@ -1082,6 +1082,10 @@ int run_mma_path(LayerParams& p, const Dims& s, const WsLayout& w, uint8_t* ws, 
 // Raises a kernel's dynamic shared-memory limit on the current device, once per
 // (kernel, device): for the kernels of the other translation units.
 cudaError_t flint_ensure_smem(const void* kern) { return ensure_smem(kern); }
+int flint_encode_map_sw128(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
+                           const cuuint64_t* strides, const cuuint32_t* box) {
+  return encode_map(m, dt, rank, base, dims, strides, box, true);
+}
 }  // namespace flint
 
 using namespace flint;

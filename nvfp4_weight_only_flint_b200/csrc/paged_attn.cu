@@ -8,7 +8,8 @@ extern "C" size_t flint_paged_attention_workspace_bytes(int32_t T, int32_t B, in
                                                         int32_t max_q_len) {
   if (T < 1 || B < 1 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0 || max_q_len < 1) return 0;
   const int group = n_q_heads / n_kv_heads;
-  if (group > kDecodeRows || B > 65535 || n_q_heads > 1024) return 0;
+  if (group > kDecodeRows || B > 65535 || n_q_heads > 1024 || T > (1 << 24)) return 0;
+  if (max_q_len > T) max_q_len = T;
   return static_cast<long long>(max_q_len) * group <= kDecodeRows
              ? paged_decode_workspace(B, n_kv_heads)
              : paged_chunk_workspace(T, B, n_q_heads, n_kv_heads, max_q_len);
@@ -37,8 +38,8 @@ extern "C" int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t
   if (!q || !out) return flint_fail_external(FLINT_ERR_INVALID_ARG, "flint_paged_attention: NULL pointer");
   if (!paged_aligned16(q) || !paged_aligned16(out) || !paged_aligned16(workspace))
     return flint_fail_external(FLINT_ERR_MISALIGNED, "flint_paged_attention: misaligned pointer");
-  if (max_q_len < 1)
-    return flint_fail_external(FLINT_ERR_INVALID_ARG, "flint_paged_attention: max_q_len must be at least 1");
+  if (max_q_len < 1 || n_pages < 1)
+    return flint_fail_external(FLINT_ERR_INVALID_ARG, "flint_paged_attention: max_q_len and n_pages must be at least 1");
   p.q = q;
   p.k = k_cache;
   p.v = v_cache;
@@ -51,10 +52,10 @@ extern "C" int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t
   p.Hkv = n_kv_heads;
   p.group = n_q_heads / n_kv_heads;
   p.window = window;
-  p.max_q = max_q_len < T ? max_q_len : T;
+  p.max_q = max_q_len < T ? max_q_len : T;  // as for the workspace size
   p.scale = scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return static_cast<long long>(max_q_len) * p.group <= kDecodeRows
+  return static_cast<long long>(p.max_q) * p.group <= kDecodeRows
              ? paged_decode_launch(p, cache_dtype, workspace_bytes, st)
              : paged_chunk_launch(p, cache_dtype, workspace_bytes, st);
 }

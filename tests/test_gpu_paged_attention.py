@@ -134,3 +134,98 @@ def test_decode_split_is_the_same_in_every_run_and_graph():
     call(o2, w2, side)
     torch.cuda.synchronize()
     assert torch.equal(out, o2)
+
+
+CHUNK = [([17], [17]), ([1, 3], [1, 200]), ([128], [128]), ([300], [300]), ([40], [1000]), ([33, 1, 0, 150, 1], [33, 2000, 5, 700, 64]),
+         ([5], [3001]), ([513, 700], [900, 701])]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("case", range(len(CHUNK)))
+def test_chunk_lengths(case, e4m3):
+    new, kv = CHUNK[case]
+    b = R.Paged(200 + case, new, kv, 8, 1, 16, e4m3)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    R.check_attention(R.run_attention(b, status=st), b, what=str((new, kv)))
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv,page", [(1, 1, 16), (3, 3, 32), (14, 2, 64), (16, 1, 128), (12, 4, 1024), (26, 2, 256),
+                                         (32, 4, 64)])
+def test_chunk_head_layouts(hq, hkv, page, e4m3):
+    b = R.Paged(hq + page, [150, 1, 20], [150, 700, 333], hq, hkv, page, e4m3)
+    R.check_attention(R.run_attention(b), b, what=f"{hq}/{hkv}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window", [1, 100, 128, 700])
+def test_chunk_window(window, e4m3):
+    b = R.Paged(window, [200, 1, 50], [200, 900, 1333], 16, 2, 16, e4m3)
+    R.check_attention(R.run_attention(b, window), b, window, what=f"window {window}")
+
+
+def test_chunk_peaked_scores():
+    # the running maximum moves by far more than the rescale threshold
+    for e4m3 in (False, True):
+        b = R.Paged(50, [70, 9], [2000, 200], 8, 1, q_gain=5.0, e4m3=e4m3)
+        R.check_attention(R.run_attention(b), b, what=f"peaked, e4m3 {e4m3}")
+
+
+def test_chunk_split_over_keys():
+    # one short piece of a long sequence: its key tiles go to many CTAs and are joined
+    for e4m3 in (False, True):
+        b = R.Paged(90, [40, 2], [20_000, 9000], 16, 2, 64, e4m3)
+        R.check_attention(R.run_attention(b), b, what=f"split, e4m3 {e4m3}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunk_invalid(e4m3):
+    _invalid([20, 37, 3, 9], [20, 80, 100, 33], e4m3)
+
+
+def test_chunk_more_tokens_than_announced():
+    b = R.Paged(70, [20, 60, 1], [30, 90, 30], 8, 2, 16)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = R.run_attention(b, status=st, max_q=40)
+    assert int(st.item()) == fm.FLINT_DEVCHECK_INDEX
+    assert (out[20:80] == 0).all()
+    out[20:80] = R.attention(b)[20:80]
+    R.check_attention(out, b)
+
+
+def test_chunk_is_the_same_in_every_run_and_graph():
+    b = R.Paged(80, [300, 17, 1, 90], [900, 17, 4000, 2500], 16, 2, 32)
+    c = b.cuda
+    dev = [c(x) for x in (b.q, b.q_start, b.kv_len, b.table, b.k, b.v)]
+    ws = torch.empty(fm.flint_paged_attention_workspace_bytes(b.T, b.B, 16, 2, 300), dtype=torch.uint8, device="cuda")
+    out = torch.empty((b.T, 16, R.DH), dtype=torch.bfloat16, device="cuda")
+
+    def call(o=out, w=ws, stream=None):
+        fm.flint_paged_attention(dev[0], b.T, dev[1], dev[2], b.B, dev[3], b.max_pages, 32, b.n_pages, dev[4], dev[5],
+                                 fm.FLINT_KV_BF16, None, None, 16, 2, 300, 0, R.DH ** -0.5, o, w, stream=stream)
+    call()
+    torch.cuda.synchronize()
+    first = out.clone()
+    R.check_attention(first.cpu().double(), b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    b.kv = [880, 17, 1, 2400]
+    dev[2].copy_(torch.tensor(b.kv, dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    b.table = dev[3].cpu()
+    R.check_attention(out.cpu().double(), b)
+    side = torch.cuda.Stream()
+    o2, w2 = torch.empty_like(out), torch.empty_like(ws)
+    side.wait_stream(torch.cuda.current_stream())
+    call()
+    call(o2, w2, side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, o2)

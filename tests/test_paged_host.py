@@ -68,12 +68,13 @@ def test_attention_arguments(L):
     assert _attn(L, hq=2048, hkv=128) == -2
     assert _attn(L, B=65536) == -2
     assert _attn(L, max_q=0) == -1
+    assert _attn(L, pages=0) == -1
     assert _attn(L, window=-1) == -1
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert _attn(L, scale=s) == -1
     assert _attn(L, T=0) == 0
     assert _attn(L, B=0) == 0
-    for mq in (1, 2):
+    for mq in (1, 2, 3, 100):
         need = fm.flint_paged_attention_workspace_bytes(4, 2, 32, 4, mq)
         assert need > 0
         assert _attn(L, max_q=mq, ws_bytes=need - 1) == -4
