@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 
+from .build import MARSHAL as _MARSHAL_PATH
 from .build import SO as _SO_PATH
 
 __all__ = [
@@ -181,22 +182,27 @@ def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _checked(**tensors):
-    """Refuses tensors that the kernels would read wrongly: strided ones, and
-    ones on another device than the current one (whose stream the call takes).
-    Each is (tensor, bytes the call reads or writes)."""
-    import torch
-    for name, (t, need) in tensors.items():
-        if t is None or isinstance(t, int):
-            continue
-        if not t.is_cuda:
-            raise FlintError(-1, f"{name}: expected a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise FlintError(-1, f"{name}: on {t.device}, the current device is {torch.cuda.current_device()}")
-        if not t.is_contiguous():
-            raise FlintError(-1, f"{name}: not contiguous")
-        if _nbytes(t) < need:
-            raise FlintError(-1, f"{name}: {_nbytes(t)} bytes, {need} needed")
+_native = None
+
+
+def _marshal():
+    """The marshalling module of the per-step serving calls (csrc/marshal.cpp)."""
+    global _native
+    if _native is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (the module links against its libraries)
+        lib()
+        if not os.path.exists(_MARSHAL_PATH):
+            raise FlintError(-5, f"{_MARSHAL_PATH} is missing: run nvfp4_weight_only_flint_b200.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", _MARSHAL_PATH)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_marshal", _MARSHAL_PATH,
+                                                                                     loader=loader))
+        loader.exec_module(mod)
+        mod.set_error(FlintError)
+        _native = mod
+    return _native
 
 
 def flint_last_error() -> str:
@@ -338,33 +344,15 @@ def flint_ep_combine(y, pair_pos, T: int, slots: int, d: int, residual, out, str
                                   _stream(stream)))
 
 
-def _check_paged(T, n_q_heads, n_kv_heads, q_start, kv_len, B, block_table, max_pages, page_size, n_pages, cache_dtype,
-                 k_scale, v_scale, k_cache, v_cache, status, head_dim):
-    T, B, mp = max(int(T), 0), max(int(B), 0), max(int(max_pages), 0)
-    pool = max(int(n_pages), 0) * max(int(page_size), 0) * int(n_kv_heads) * int(head_dim) * (
-        1 if cache_dtype == FLINT_KV_E4M3 else 2)
-    scales = 4 * int(n_kv_heads) if cache_dtype == FLINT_KV_E4M3 else 0
-    live = T > 0 and B > 0
-    _checked(q_start=(q_start, 4 * (B + 1) * live), kv_len=(kv_len, 4 * B * live),
-             block_table=(block_table, 4 * B * mp * live), k_cache=(k_cache, pool), v_cache=(v_cache, pool),
-             k_scale=(k_scale, scales), v_scale=(v_scale, scales), status=(status, 4))
-
-
+# The serving calls check their tensors (contiguous, on the current device, large enough) and raise FlintError
+# before anything is launched; see csrc/marshal.cpp.
 def flint_qk_norm_rope_paged_kv(qkv, T: int, n_q_heads: int, n_kv_heads: int, q_norm_w, k_norm_w, cos_sin,
                                 max_pos: int, rope: bool, eps: float, q_start, kv_len, B: int, block_table,
                                 max_pages: int, page_size: int, n_pages: int, cache_dtype: int, k_scale, v_scale,
                                 q_out, k_cache, v_cache, status=None, head_dim: int = 128, stream=None) -> None:
-    _check_paged(T, n_q_heads, n_kv_heads, q_start, kv_len, B, block_table, max_pages, page_size, n_pages, cache_dtype,
-                 k_scale, v_scale, k_cache, v_cache, status, head_dim)
-    row = 2 * max(int(T), 0) * int(head_dim)
-    _checked(qkv=(qkv, row * (n_q_heads + 2 * n_kv_heads)), q_out=(q_out, row * n_q_heads),
-             q_norm_w=(q_norm_w, 2 * head_dim), k_norm_w=(k_norm_w, 2 * head_dim),
-             cos_sin=(cos_sin, 4 * head_dim * max(int(max_pos), 0) if rope else 0))
-    _check(lib().flint_qk_norm_rope_paged_kv(
-        _ptr(qkv), int(T), int(n_q_heads), int(n_kv_heads), int(head_dim), _ptr(q_norm_w), _ptr(k_norm_w),
-        _ptr(cos_sin), int(max_pos), int(bool(rope)), float(eps), _ptr(q_start), _ptr(kv_len), int(B),
-        _ptr(block_table), int(max_pages), int(page_size), int(n_pages), int(cache_dtype), _ptr(k_scale),
-        _ptr(v_scale), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(status), _stream(stream)))
+    (_native or _marshal()).paged_kv(qkv, T, n_q_heads, n_kv_heads, q_norm_w, k_norm_w, cos_sin, max_pos, rope, eps,
+                                     q_start, kv_len, B, block_table, max_pages, page_size, n_pages, cache_dtype,
+                                     k_scale, v_scale, q_out, k_cache, v_cache, status, head_dim, stream)
 
 
 def flint_paged_attention_workspace_bytes(T: int, B: int, n_q_heads: int, n_kv_heads: int, max_q_len: int) -> int:
@@ -376,29 +364,15 @@ def flint_paged_attention(q, T: int, q_start, kv_len, B: int, block_table, max_p
                           n_pages: int, k_cache, v_cache, cache_dtype: int, k_scale, v_scale, n_q_heads: int,
                           n_kv_heads: int, max_q_len: int, window: int, scale: float, out, workspace, status=None,
                           head_dim: int = 128, stream=None) -> None:
-    _check_paged(T, n_q_heads, n_kv_heads, q_start, kv_len, B, block_table, max_pages, page_size, n_pages, cache_dtype,
-                 k_scale, v_scale, k_cache, v_cache, status, head_dim)
-    row = 2 * max(int(T), 0) * int(head_dim) * int(n_q_heads)
-    _checked(q=(q, row), out=(out, row), workspace=(workspace, 0))
-    _check(lib().flint_paged_attention(
-        _ptr(q), int(T), _ptr(q_start), _ptr(kv_len), int(B), _ptr(block_table), int(max_pages), int(page_size),
-        int(n_pages), _ptr(k_cache), _ptr(v_cache), int(cache_dtype), _ptr(k_scale), _ptr(v_scale), int(n_q_heads),
-        int(n_kv_heads), int(head_dim), int(max_q_len), int(window), float(scale), _ptr(out), _ptr(workspace),
-        _nbytes(workspace), _ptr(status), _stream(stream)))
+    (_native or _marshal()).paged_attention(q, T, q_start, kv_len, B, block_table, max_pages, page_size, n_pages,
+                                            k_cache, v_cache, cache_dtype, k_scale, v_scale, n_q_heads, n_kv_heads,
+                                            max_q_len, window, scale, out, workspace, status, head_dim, stream)
 
 
 def flint_sample(logits, rows: int, vocab: int, row_stride: int, logits_dtype: int, temperature, top_k, top_p, min_p,
                  u, tokens, logprobs=None, status=None, stream=None) -> None:
-    r = max(int(rows), 0)
-    per_row = 4 * r
-    es = 4 if logits_dtype == FLINT_LOGITS_F32 else 2
-    _checked(logits=(logits, es * ((r - 1) * int(row_stride) + int(vocab)) if r else 0),
-             temperature=(temperature, per_row), top_k=(top_k, per_row), top_p=(top_p, per_row),
-             min_p=(min_p, per_row), u=(u, per_row), tokens=(tokens, per_row), logprobs=(logprobs, per_row),
-             status=(status, 4))
-    _check(lib().flint_sample(_ptr(logits), int(rows), int(vocab), int(row_stride), int(logits_dtype),
-                              _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(tokens),
-                              _ptr(logprobs), _ptr(status), _stream(stream)))
+    (_native or _marshal()).sample(logits, rows, vocab, row_stride, logits_dtype, temperature, top_k, top_p, min_p, u,
+                                   tokens, logprobs, status, stream)
 
 
 def flint_moe_get_status(workspace, stream=None) -> tuple[int, int]:

@@ -1,4 +1,4 @@
-"""Build libflint_moe.so in-tree with nvcc for sm_100a (B200)."""
+"""Build libflint_moe.so in-tree with nvcc for sm_100a (B200), and the Python marshalling module beside it with g++."""
 from __future__ import annotations
 
 import os
@@ -10,6 +10,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(PKG, "libflint_moe.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 # translation units, compiled in parallel and linked into one shared library
 SOURCES = ["flint_moe.cu", "tok1.cu", "tokn.cu", "lmhead.cu", "attn.cu", "attn_decode.cu", "ep.cu",
@@ -24,7 +26,36 @@ def _inputs():
     return files
 
 
+def _build_marshal(force: bool, verbose: bool) -> None:
+    """The extension module needs torch's headers and links against torch and libflint_moe.so (found beside it)."""
+    header = os.path.join(INCLUDE, "flint_moe.h")
+    if not force and os.path.exists(MARSHAL) and all(
+            os.path.getmtime(f) <= os.path.getmtime(MARSHAL) for f in (MARSHAL_SRC, header)):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{cuda}", *[f"-I{d}" for d in include_paths()], MARSHAL_SRC,
+           "-o", tmp, *[f"-L{d}" for d in library_paths()], f"-L{PKG}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python", "-l:libflint_moe.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    so = _build_library(force, verbose)
+    _build_marshal(force, verbose)
+    return so
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and os.path.exists(SO):
         so_time = os.path.getmtime(SO)
         if all(os.path.getmtime(f) <= so_time for f in _inputs()):
