@@ -1,9 +1,10 @@
 """Sampling against its 64-bit form, row by row: every filter alone and together, vocabularies from one token to more
 than shared memory holds, ties, masked rows, infinities, NaN, extreme temperatures, strides, both logit types.
 
-Tokens have to be equal: the kernel's masses are exact sums of weights off by 2^-45, so a token could differ only where
-u, top_p or min_p falls within 150,144 * 2^-45 < 2^-27 of a border, which these seeds do not meet. Log-probabilities:
-fp32 rounding of a double (2^-24 relative) plus the 2^-27 of the total."""
+Tokens have to be equal: each weight is right to 2^-28 of itself and the sums are exact, so a token could differ only
+where u, top_p or min_p falls within 2^-28 of a border (less than 1e-6 a row), which these seeds do not meet.
+Log-probabilities: the ratio of a weight and a sum, each right to 2^-28 (2^-27 absolute in the logarithm), and the fp32
+rounding of the result (2^-24 relative)."""
 import math
 
 import pytest
@@ -66,9 +67,17 @@ def test_sample_filters(V, dtype):
 
 
 def test_sample_larger_than_shared_memory():
-    V = 400_003  # above what eight CTAs hold: the shares are read again from global memory
+    V = 900_001  # above what eight CTAs hold
     kinds = [(1.0, 0, 1.0, 0.0), (0.8, 50, 0.9, 0.0), (1.0, 0, 0.95, 0.0), (1.0, 0, 1.0, 0.1)]
     _check(_logits(7, 4, V), *[[q[i] for q in kinds] for i in range(4)], _u(8, 4))
+
+
+@pytest.mark.parametrize("rows,V", [(37, 65_600), (60, 70_001), (2, 376_832), (2, 376_833), (3, 400_003)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sample_shares_held_and_read_again(rows, V, dtype):
+    # up to 376,832 tokens (8 CTAs of 47,104) the row is held in shared memory
+    kinds = [(1.0, 0, 1.0, 0.0), (0.8, 50, 0.9, 0.0), (1.0, 0, 0.95, 0.0), (1.0, 0, 1.0, 0.1), (0.0, 0, 1.0, 0.0)]
+    _check(_logits(rows, rows, V, dtype), *[[kinds[r % 5][i] for r in range(rows)] for i in range(4)], _u(9, rows))
 
 
 def test_sample_defaults_and_no_logprobs():
@@ -132,12 +141,38 @@ def test_sample_masked_rows_and_infinities():
             assert int(tok[r]) == want, r
             assert abs(float(lp[r]) - lw) <= 2 ** -23 * abs(lw) + 2 ** -26
     assert _run(x, [0.0] * 7, u=u)[0].tolist()[1:3] == [4321, 100]
+    # the same where the row is not held in shared memory
+    long = x[2:3].repeat(8, 80)  # 400,000 tokens
+    tok, lp = _run(long, [0.9] * 8, [0] * 8, [1.0] * 8, [0.0] * 8, _u(13, 8))
+    want = {100 + V * i for i in range(80)} | {200 + V * i for i in range(80)}
+    assert set(tok.tolist()) <= want and abs(float(lp[0]) + math.log(160)) < 1e-6
 
 
-@pytest.mark.parametrize("t", [1e-30, 1e-3, 0.05, 20.0, 1e6])
+@pytest.mark.parametrize("t", [1e-44, 1e-30, 1e-3, 0.05, 20.0, 1e6])
 def test_sample_extreme_temperatures(t):
     x = _logits(21, 4, 20_000)
     _check(x, [t] * 4, [0, 500, 0, 0], [1.0, 0.9, 0.9, 1.0], [0.0, 0.0, 0.0, 0.3], _u(22, 4))
+
+
+@pytest.mark.parametrize("k", [255, 256, 257, 511, 512, 513, 1024, 1025, 3000])
+def test_sample_prefix_sizes(k):
+    # prefixes on both sides of every form's limit: counted ranks, sorted, narrowed
+    x = _logits(k, 6, 20_000, spread=3.0)
+    _check(x, [1.0] * 6, [k] * 6, [1.0, 0.9, 0.999, 1.0, 0.5, 1.0], [0.0, 0.0, 0.0, 0.01, 0.0, 1e-6], _u(k, 6))
+
+
+@pytest.mark.parametrize("spread", [0.01, 0.5, 6.0, 40.0])
+def test_sample_flat_and_steep_rows(spread):
+    # top-p ends within the near bins, below them, among one bin's many tokens
+    x = torch.randn((8, 30_000), generator=torch.Generator().manual_seed(5)) * spread
+    _check(x, [1.0] * 8, [0, 0, 0, 0, 700, 300, 50, 29_999], [0.1, 0.5, 0.9, 0.9999999, 0.9, 0.5, 0.99, 0.3], [0.0] * 8,
+           _u(6, 8))
+
+
+def test_sample_top_k_of_crowded_bins():
+    # thousands of tokens within a bin of the k-th: the gather is given up
+    x = torch.full((4, 50_000), -1.0) + torch.rand((4, 50_000), generator=torch.Generator().manual_seed(9)) * 0.01
+    _check(x, [1.0] * 4, [50, 500, 5, 100], [1.0, 0.9, 0.5, 1.0], [0.0] * 4, _u(10, 4))
 
 
 def test_sample_filters_at_their_ends():
