@@ -260,7 +260,7 @@ struct Item {
 
 template <bool kE4M3>
 struct Ctl {
-  uint64_t q_full[2], q_empty[2], qc_full[2], kv_full[5], kv_empty[5], raw_full[3], raw_empty[3], s_full[2], p_full[2],
+  uint64_t q_full[2], q_empty[2], qc_full[2], kv_full[5], kv_empty[5], raw_full[3], raw_empty[3], s_full[2], p_full[2][2],
       o_done[2], it_full[2], it_empty[2];
   Item item[2];
   uint32_t tmem;
@@ -270,7 +270,7 @@ struct Ctl {
 
 template <bool kE4M3>
 constexpr size_t smem_bytes() {
-  return 1024 + 2 * kTileBytes + Cfg<kE4M3>::kStages * kTileBytes + Cfg<kE4M3>::kRaw * kRawBytes +
+  return 2 * kTileBytes + Cfg<kE4M3>::kStages * kTileBytes + Cfg<kE4M3>::kRaw * kRawBytes +
          sizeof(Ctl<kE4M3>);
 }
 static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory");
@@ -281,14 +281,33 @@ template <int kRegs>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Two fp32 at a time (sm_100's packed arithmetic).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <bool kE4M3>
 __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
     k_paged_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, PagedAttnParams p, Ws w, int rows_per_slot) {
   using C = Cfg<kE4M3>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-  uint8_t* sq = base;
+  extern __shared__ __align__(1024) uint8_t sq[];  // the 128-byte swizzle repeats every 1024 bytes
   uint8_t* skv = sq + 2 * kTileBytes;
   uint8_t* sraw = skv + C::kStages * kTileBytes;
   Ctl<kE4M3>& ctl = *reinterpret_cast<Ctl<kE4M3>*>(sraw + C::kRaw * kRawBytes);
@@ -302,7 +321,8 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
       mbar_init(&ctl.q_empty[i], 1);
       mbar_init(&ctl.qc_full[i], 128);
       mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.p_full[i], 128);
+      mbar_init(&ctl.p_full[i][0], 128);
+      mbar_init(&ctl.p_full[i][1], 128);
       mbar_init(&ctl.o_done[i], 1);
       mbar_init(&ctl.it_full[i], 1);
       mbar_init(&ctl.it_empty[i], 1 + 8 + (kE4M3 ? 4 : 0));
@@ -415,15 +435,18 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
           }
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const f32x2 c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+        f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t r[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float a = exp2_ftz(fmaf(s[32 * i + 2 * j], c, -mc)), b = exp2_ftz(fmaf(s[32 * i + 2 * j + 1], c, -mc));
-            sum[(2 * j) & 3] += a;
-            sum[(2 * j + 1) & 3] += b;
+            float a, b;
+            unpack2(fma2(pack2(s[32 * i + 2 * j], s[32 * i + 2 * j + 1]), c2, mc2), a, b);
+            a = exp2_ftz(a);
+            b = exp2_ftz(b);
+            sum[j & 1] = add2(sum[j & 1], pack2(a, b));
             if constexpr (kE4M3) {
               r[j] = pack_f16x2(a, b);
             } else {
@@ -432,11 +455,19 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
             }
           }
           tmem_st16(ts + 16 * i, r);
+          if (i == 1) {  // P V of the first 64 keys starts while the others are weighed (prompt of 8,192: 524 -> 512 us)
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&ctl.p_full[t][0]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&ctl.p_full[t]);
+        mbar_arrive(&ctl.p_full[t][1]);
+        float s0, s1, s2, s3;
+        unpack2(sum[0], s0, s1);
+        unpack2(sum[1], s2, s3);
+        l += (s0 + s1) + (s2 + s3);
         ++cnt;
       }
       if (!ok) break;
@@ -496,13 +527,13 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
       }
       __syncwarp();
     };
-    auto issue_o = [&](int t, uint32_t v_addr, bool acc) {
+    auto issue_o = [&](int t, int half, uint32_t v_addr, bool acc) {
       if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k, sw128_mn_desc(v_addr + k * 2048, kHalfBytes), idesc_o,
-                     acc || k > 0);
-        mma_commit(&ctl.o_done[t]);
+        for (int k = 0; k < 4; ++k)
+          mma_f16_ts(tmem + 256 + t * 128, tmem + t * 128 + 32 * half + 8 * k,
+                     sw128_mn_desc(v_addr + (4 * half + k) * 2048, kHalfBytes), idesc_o, acc || half + k > 0);
+        if (half == 1) mma_commit(&ctl.o_done[t]);
       }
       __syncwarp();
     };
@@ -540,10 +571,13 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
           }
         }
         for (int t = 0; t < nt; ++t) {
-          if (!(ok = mma_wait(&ctl.p_full[t], cnt[t] & 1, ab, status))) break;
+          for (int half = 0; half < 2 && ok; ++half) {
+            if (!(ok = mma_wait(&ctl.p_full[t][half], cnt[t] & 1, ab, status))) break;
+            tc_fence_after();
+            issue_o(t, half, stage(vi), j > 0);
+          }
+          if (!ok) break;
           ++cnt[t];
-          tc_fence_after();
-          issue_o(t, stage(vi), j > 0);
           if (j + 1 < nk) {
             if (t == 0 && !wait_kv(ki)) break;
             tc_fence_after();
