@@ -8,11 +8,11 @@ extern "C" size_t flint_paged_attention_workspace_bytes(int32_t T, int32_t B, in
                                                         int32_t max_q_len) {
   if (T < 1 || B < 1 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0 || max_q_len < 1) return 0;
   const int group = n_q_heads / n_kv_heads;
-  if (group > kDecodeRows || B > 65535 || n_q_heads > 1024 || T > (1 << 24)) return 0;
+  if (group > kDecodeRows || B > 32768 || n_q_heads > 1024 || T > (1 << 24)) return 0;
   if (max_q_len > T) max_q_len = T;
   return static_cast<long long>(max_q_len) * group <= kDecodeRows
              ? paged_decode_workspace(B, n_kv_heads)
-             : paged_chunk_workspace(T, B, n_q_heads, n_kv_heads, max_q_len);
+             : paged_chunk_workspace(n_q_heads, n_kv_heads, max_q_len);
 }
 
 extern "C" int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t* q_start, const int32_t* kv_len,
@@ -27,9 +27,9 @@ extern "C" int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t
     return flint_fail_external(FLINT_ERR_INVALID_ARG, "flint_paged_attention: bad sizes");
   if (n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > kDecodeRows)
     return flint_fail_external(FLINT_ERR_UNSUPPORTED_SHAPE, "n_q_heads / n_kv_heads must be an integer <= 16");
-  if (B > 65535 || n_q_heads > 1024 || T > (1 << 24))
+  if (B > 32768 || n_q_heads > 1024 || T > (1 << 24))
     return flint_fail_external(FLINT_ERR_UNSUPPORTED_SHAPE,
-                               "at most 65535 sequences, 1024 query heads and 2^24 new tokens");
+                               "at most 32768 sequences, 1024 query heads and 2^24 new tokens");
   PagedAttnParams p{};
   const int rc = paged_batch(&p.b, "flint_paged_attention", T, q_start, kv_len, B, block_table, max_pages, page_size,
                              n_pages, cache_dtype, k_cache, v_cache, k_scale, v_scale);

@@ -41,7 +41,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 int paged_decode_launch(const PagedAttnParams& p, int cache_dtype, size_t ws_bytes, cudaStream_t st);
 size_t paged_decode_workspace(int B, int n_kv_heads);
 int paged_chunk_launch(const PagedAttnParams& p, int cache_dtype, size_t ws_bytes, cudaStream_t st);
-size_t paged_chunk_workspace(int T, int B, int n_q_heads, int n_kv_heads, int max_q);
+size_t paged_chunk_workspace(int n_q_heads, int n_kv_heads, int max_q);
 
 // New tokens times query heads per kv head that one 16-row register tile
 // holds: such calls take the decode kernel, others the chunk kernel.

@@ -4,14 +4,24 @@
 // happened": 8K-token prefill; heads from "Recursive Flint: 125 tok/s on an M4
 // Pro", architecture table).
 //
-// k_chunk_plan (one CTA) turns the lengths it finds on the device into a work
-// list; k_paged_chunk (one CTA per SM) takes (entry, kv head) items off it;
-// k_chunk_combine joins the entries that were split over keys.
+// k_paged_chunk works through pieces: a pair of query tiles against a run of
+// 128-key tiles. A query tile is 128 rows = floor(128 / group) tokens x the
+// group of query heads that share the kv head: K and V are fetched once for 2 x
+// 128 rows, and a causal edge cuts at most 128 / group tokens. All tile pairs of
+// all sequences in turn, each as long as its key tiles and two more for the fill
+// and drain of the pipeline, form one line that 148 / Hkv CTAs per kv head cut
+// into equal parts; each CTA finds its part from the lengths (a scan over the
+// sequences and one over the tile pairs, 1-2 us), so a captured graph stays
+// balanced when the lengths change. A pair that spans parts leaves partials, at
+// most two per CTA, that k_chunk_combine joins. (A list of whole pairs made by a
+// kernel of its own and taken longest first: 1,024 tokens over 31,000 601 us
+// against 503, since 128 items do not fill 148 CTAs, and a mixed step 66 us
+// against 60, 10 of them the list.) Where pairs are many and short beside a part
+// (deal_whole), they are dealt out whole instead, from the last one of the line
+// (a prompt's longest) and back and forth: a prompt of 8,192 tokens 512 us
+// against 550, without partials.
 //
-// An item is a pair of query tiles against a run of 128-key tiles. A query tile
-// is 128 rows = floor(128 / group) tokens x the group of query heads that share
-// the kv head: K and V are fetched once for 2 x 128 rows, and a causal edge
-// cuts at most 128 / group tokens. Per key tile and query tile
+// Per key tile and query tile
 //   S = Q K^T     tcgen05.mma, both operands in shared memory (TMA, 128-byte swizzle)
 //   P = 2^(S c - m c)   by the tile's own warpgroup: thread = row, S read from
 //                 tensor memory into registers, P rounded and written back over S
@@ -27,6 +37,8 @@
 // Keys past a sequence's end: S is masked by column, and V rows are zeroed in
 // shared memory, so whatever unused cache rows hold stays out of the sums.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "paged_attn.cuh"
 #include "tcgen05.cuh"
@@ -44,7 +56,9 @@ constexpr int kTileBytes = kTile * kDh * 2;
 constexpr int kHalfBytes = kTileBytes / 2; // 64 dims of a tile
 constexpr int kRawBytes = kTile * kDh;
 constexpr int kCtas = 148;
-constexpr int kMaxSplit = 4 * kCtas;       // partial slots over all kv heads
+constexpr int kFill = 2;                   // length of a tile pair on the line beyond its key tiles
+constexpr int kMinPart = 6;                // no part is shorter
+constexpr int kMaxSeqs = 32768;            // the scan over sequences lives in the stages' shared memory
 constexpr float kRescale = 8.f;            // log2 units
 
 template <bool kE4M3>
@@ -55,56 +69,37 @@ struct Cfg {
   static constexpr int kFullCount = kE4M3 ? 128 : 1;
 };
 
-// One tile pair of one sequence; entries add a key range and a partial slot.
-struct Tile {
-  int s, tok0, kt0, kt1;
-};
-struct Entry {
-  int s, tok0, kt0, kt1, slot, pad0, pad1, pad2;  // slot -1: the whole range
-};
+// A tile pair cut by part boundaries: its pieces are in parts first .. last.
 struct Split {
-  int s, tok0, slot, parts;
-};
-struct Plan {
-  int n_entries, n_split, counter, flags;
+  int s, tok0, first, last;  // s -1: none
 };
 struct Ws {
-  Plan* plan;
-  int* tile_off;  // [B + 1]
-  Tile* tiles;
-  Entry* entries;
-  Split* splits;
-  float* ml;      // [slot][2 * 128][2]
-  float* po;      // [slot][2 * 128][128]
+  int* flags;     // stands in for a null status
+  Split* splits;  // [parts]: the pair that part leaves unfinished
+  float* ml;      // [slot][rows][2]: maximum (log2 units), sum
+  float* po;      // [slot][rows][128]
 };
 __host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-__host__ __device__ inline int split_cap(int Hkv) { return Hkv >= kMaxSplit ? 1 : kMaxSplit / Hkv; }
-// Tile pairs of T tokens in B sequences, at most.
-__host__ __device__ inline size_t max_pairs(int T, int B, int group) {
-  return static_cast<size_t>(T) / (2 * (kTile / group)) + B;
-}
+__host__ __device__ inline int parts_per_head(int Hkv) { return Hkv >= kCtas ? 1 : kCtas / Hkv; }
 __host__ __device__ inline int slot_rows(int max_q, int group) {
-  const long long r = static_cast<long long>(max_q) * group;
-  return r >= 2 * kTile ? 2 * kTile : r > kTile ? 2 * kTile : kTile;
+  return static_cast<long long>(max_q) * group > kTile ? 2 * kTile : kTile;
 }
-__host__ __device__ inline size_t carve(Ws* w, char* ws, int T, int B, int Hkv, int group, int rows) {
+__host__ __device__ inline size_t carve(Ws* w, char* ws, int Hkv, int rows) {
   char* p = ws;
-  w->plan = reinterpret_cast<Plan*>(p);
+  w->flags = reinterpret_cast<int*>(p);
   p += 256;
-  w->tile_off = reinterpret_cast<int*>(p);
-  p += up256((static_cast<size_t>(B) + 1) * sizeof(int));
-  const size_t nt = max_pairs(T, B, group), sc = split_cap(Hkv);
-  w->tiles = reinterpret_cast<Tile*>(p);
-  p += up256(nt * sizeof(Tile));
-  w->entries = reinterpret_cast<Entry*>(p);
-  p += up256((nt + sc) * sizeof(Entry));
+  const size_t parts = parts_per_head(Hkv), slots = parts * Hkv * 2;
   w->splits = reinterpret_cast<Split*>(p);
-  p += up256(sc * sizeof(Split));
+  p += up256(parts * sizeof(Split));
   w->ml = reinterpret_cast<float*>(p);
-  p += up256(sc * Hkv * rows * 2 * sizeof(float));
+  p += up256(slots * rows * 2 * sizeof(float));
   w->po = reinterpret_cast<float*>(p);
-  p += sc * Hkv * rows * kDh * sizeof(float);
+  p += slots * rows * kDh * sizeof(float);
   return static_cast<size_t>(p - ws);
+}
+// Piece of part i: the pair ends there (0) or goes on (1).
+__device__ __forceinline__ size_t slot_of(int part, int Hkv, int g, bool goes_on) {
+  return (static_cast<size_t>(part) * Hkv + g) * 2 + (goes_on ? 1 : 0);
 }
 
 __device__ __forceinline__ PagedSeq chunk_seq(const PagedAttnParams& p, int s, bool* bad) {
@@ -116,141 +111,147 @@ __device__ __forceinline__ PagedSeq chunk_seq(const PagedAttnParams& p, int s, b
   return q;
 }
 
-// ------------------------------------------------------------------- the plan
-constexpr int kPlanThreads = 1024;
+// ------------------------------------------------------------------- the line
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Exclusive scan of one value per thread; *total is the sum.
-__device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
+// Key tiles [kt0, kt1) that the tile pair from token tok0 of a sequence attends.
+struct Keys {
+  int kt0, kt1;
+  __device__ __forceinline__ int length() const { return kt1 - kt0 + kFill; }
+};
+__device__ __forceinline__ Keys pair_keys(const PagedSeq& q, int tok0, int pair, int window) {
+  const int end = q.kv - q.n + min(q.n, tok0 + pair);
+  const int first = window > 0 ? max(0, q.kv - q.n + tok0 - window + 1) : 0;
+  return Keys{first / kTile, (end + kTile - 1) / kTile};
+}
+__device__ __forceinline__ int pairs_of(const PagedSeq& q, int pair) { return q.kv > 0 ? (q.n + pair - 1) / pair : 0; }
+
+// Where a part of the line begins.
+constexpr int kDealSeqs = 64;  // sequences whose first pairs are kept for it
+struct Start {
+  long long base, total;  // of the pair that holds the part's first place; length of the line
+  int s, tok0;
+  int n_pairs, longest, deal;
+  int first_pair[kDealSeqs];
+};
+
+// Exclusive scan of one value per thread over the block; *total is the sum.
+template <int kThreads>
+__device__ __forceinline__ long long block_scan(long long v, long long* s_warp, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  long long inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
   __syncthreads();
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    all += s_warp[w];
+  long long before = 0, all = 0;
+#pragma unroll 4
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long x = s_warp[w];
+    if (w < warp) before += x;
+    all += x;
   }
   *total = all;
   return before + inc - v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) k_chunk_plan(PagedAttnParams p, Ws w) {
-  __shared__ int s_warp[kPlanThreads / 32];
-  __shared__ unsigned long long s_sum[4];
-  __shared__ int s_max;
+// Whole pairs, dealt back and forth: four or more a CTA, none longer than a
+// third of a part.
+__device__ __forceinline__ bool deal_whole(int B, long long n_pairs, int longest, long long total, int n_parts) {
+  return B <= kDealSeqs && n_pairs >= 4ll * n_parts && 3ll * longest * n_parts <= total;
+}
+
+// All threads of the CTA. first_pair: scratch for B + 1 ints. Parts: place i of
+// n is total i / n; n is chosen here so that no part is shorter than kMinPart.
+template <int kThreads>
+__device__ __forceinline__ void find_start(const PagedAttnParams& p, int part, int* n_parts, int* first_pair,
+                                           long long* s_warp, Start* start) {
   const int tid = threadIdx.x;
-  pdl_trigger();
-  const int pair = 2 * (kTile / p.group);  // tokens of a tile pair
-  if (tid < 4) s_sum[tid] = 0;
-  if (tid == 0) s_max = 0;
-  // tile pairs of each sequence
-  int n_tiles = 0;
-  for (int s0 = 0; s0 < p.b.B; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    int c = 0;
-    if (s < p.b.B) {
-      bool bad;
-      const PagedSeq q = chunk_seq(p, s, &bad);
-      if (bad && p.status != nullptr) atomicOr(p.status, FLINT_DEVCHECK_INDEX);
-      c = q.kv > 0 ? (q.n + pair - 1) / pair : 0;
-    }
-    int tot;
-    const int at = n_tiles + block_scan(c, s_warp, &tot);
-    if (s < p.b.B) w.tile_off[s] = at;
-    n_tiles += tot;
+  const int pair = 2 * (kTile / p.group);
+  const int per = (p.b.B + kThreads - 1) / kThreads;
+  const int sb = min(p.b.B, tid * per), se = min(p.b.B, sb + per);
+  long long mine = 0, n_pairs;
+  if (tid == 0) start->longest = 0;
+  for (int s = sb; s < se; ++s) {
+    bool bad;
+    const PagedSeq q = chunk_seq(p, s, &bad);
+    if (bad && blockIdx.x == 0 && p.status != nullptr) atomicOr(p.status, FLINT_DEVCHECK_INDEX);
+    mine += pairs_of(q, pair);
   }
-  // overlapping token ranges could promise more tiles than the list holds
-  const int cap = static_cast<int>(max_pairs(p.b.T, p.b.B, p.group));
-  if (n_tiles > cap) {
-    n_tiles = cap;
-    if (tid == 0 && p.status != nullptr) atomicOr(p.status, FLINT_DEVCHECK_INDEX);
+  long long at = block_scan<kThreads>(mine, s_warp, &n_pairs);
+  // overlapping token ranges could promise more pairs than 32 bits count
+  if (n_pairs > (1 << 30)) n_pairs = 0;
+  for (int s = sb; s < se; ++s) {
+    bool bad;
+    first_pair[s] = static_cast<int>(min(at, 1ll << 30));
+    at += pairs_of(chunk_seq(p, s, &bad), pair);
   }
   __syncthreads();
-  unsigned long long sum = 0;
-  int longest = 0;
-  for (int i = tid; i < n_tiles; i += kPlanThreads) {
-    int lo = 0, hi = p.b.B;  // the last sequence whose tiles start at or before i
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (w.tile_off[mid] <= i) lo = mid;
+  // each thread a run of pairs: their length
+  const int q_per = static_cast<int>((n_pairs + kThreads - 1) / kThreads);
+  const int i0 = static_cast<int>(min(n_pairs, static_cast<long long>(tid) * q_per));
+  const int i1 = static_cast<int>(min(n_pairs, static_cast<long long>(i0) + q_per));
+  int s0 = 0;
+  if (i0 < i1) {
+    int hi = p.b.B;  // the last sequence whose pairs start at or before i0
+    while (hi - s0 > 1) {
+      const int mid = (s0 + hi) >> 1;
+      if (first_pair[mid] <= i0) s0 = mid;
       else hi = mid;
     }
+  }
+  // f(sequence, first token, length) over the run, until it returns true
+  auto walk = [&](auto&& f) {
+    int s = s0;
     bool bad;
-    const PagedSeq q = chunk_seq(p, lo, &bad);
-    const int tok0 = (i - w.tile_off[lo]) * pair;
-    const int last = min(q.n, tok0 + pair);
-    const int end = q.kv - q.n + last;
-    const int first = p.window > 0 ? max(0, q.kv - q.n + tok0 - p.window + 1) : 0;
-    const Tile t{lo, tok0, first / kTile, (end + kTile - 1) / kTile};
-    w.tiles[i] = t;
-    sum += t.kt1 - t.kt0;
-    longest = max(longest, t.kt1 - t.kt0);
-  }
-  if (sum != 0) atomicAdd(&s_sum[0], sum);
-  if (longest != 0) atomicMax(&s_max, longest);
-  __syncthreads();
-  // Run length: whole ranges, or pieces of about one or half a CTA's even
-  // share. Estimated time in key tiles: the even share of all work, 2 tiles of
-  // fill and drain per item, 2 more per piece of a split, and half the longest
-  // item (the tail of the last one).
-  const int Hkv = p.Hkv;
-  const unsigned long long W = s_sum[0] * Hkv;
-  const int even = static_cast<int>(min((W + kCtas - 1) / kCtas, 1ull << 24));
-  const int c1 = max(4, even), c2 = max(4, (even + 1) / 2);
-  unsigned long long n1 = 0, n2 = 0;
-  for (int i = tid; i < n_tiles; i += kPlanThreads) {
-    const int len = w.tiles[i].kt1 - w.tiles[i].kt0;
-    if (len > c1) n1 += (len + c1 - 1) / c1;
-    if (len > c2) n2 += (len + c2 - 1) / c2;
-  }
-  if (n1 != 0) atomicAdd(&s_sum[1], n1);
-  if (n2 != 0) atomicAdd(&s_sum[2], n2);
-  __syncthreads();
-  const int sc = split_cap(Hkv);
-  auto est = [&](unsigned long long pieces, int len) {
-    return (static_cast<float>(W) + Hkv * (2.f * n_tiles + 4.f * pieces)) / kCtas + 0.5f * len;
+    PagedSeq q = chunk_seq(p, s, &bad);
+    int tok = i0 < i1 ? (i0 - first_pair[s]) * pair : 0;
+    for (int i = i0; i < i1; ++i) {
+      while (q.kv <= 0 || tok >= q.n) {  // the next sequence with new tokens
+        q = chunk_seq(p, ++s, &bad);
+        tok = 0;
+      }
+      if (f(s, tok, pair_keys(q, tok, pair, p.window).length())) return;
+      tok += pair;
+    }
   };
-  int run = 1 << 30;
-  float best = est(0, s_max);
-  if (s_sum[1] > 0 && s_sum[1] <= sc && est(s_sum[1], c1) < best) {
-    best = est(s_sum[1], c1);
-    run = c1;
+  long long len = 0, total;
+  int longest = 0;
+  walk([&](int, int, int l) {
+    len += l;
+    longest = max(longest, l);
+    return false;
+  });
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if ((tid & 31) == 0 && longest != 0) atomicMax(&start->longest, longest);
+  long long base = block_scan<kThreads>(len, s_warp, &total);
+  *n_parts = static_cast<int>(min(static_cast<long long>(parts_per_head(p.Hkv)), (total + kMinPart - 1) / kMinPart));
+  if (tid == 0) {
+    start->total = total;
+    start->n_pairs = static_cast<int>(n_pairs);
+    start->deal = deal_whole(p.b.B, n_pairs, start->longest, total, *n_parts);
   }
-  if (s_sum[2] > 0 && s_sum[2] <= sc && est(s_sum[2], c2) < best) run = c2;
-  // the list, last tiles (the longest of a sequence) first
-  int n_entries = 0, n_pieces = 0, n_split = 0;
-  for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
-    const int i = n_tiles - 1 - (i0 + tid);
-    Tile t{0, 0, 0, 0};
-    int parts = 0;
-    if (i >= 0) {
-      t = w.tiles[i];
-      parts = max(1, (t.kt1 - t.kt0 + run - 1) / run);
-    }
-    const bool split = parts > 1;
-    int te, tp, ts;
-    const int e = n_entries + block_scan(parts, s_warp, &te);
-    const int slot = n_pieces + block_scan(split ? parts : 0, s_warp, &tp);
-    const int si = n_split + block_scan(split ? 1 : 0, s_warp, &ts);
-    if (i >= 0) {
-      const int len = t.kt1 - t.kt0;
-      for (int k = 0; k < parts; ++k)
-        w.entries[e + k] = Entry{t.s, t.tok0, t.kt0 + static_cast<int>(static_cast<long long>(len) * k / parts),
-                                 t.kt0 + static_cast<int>(static_cast<long long>(len) * (k + 1) / parts),
-                                 split ? slot + k : -1, 0, 0, 0};
-      if (split) w.splits[si] = Split{t.s, t.tok0, slot, parts};
-    }
-    n_entries += te;
-    n_pieces += tp;
-    n_split += ts;
+  if (tid < kDealSeqs && tid < p.b.B) start->first_pair[tid] = first_pair[tid];
+  if (part < *n_parts) {
+    const long long a = total * part / *n_parts;
+    if (a >= base && a < base + len)
+      walk([&](int s, int tok, int l) {
+        if (a < base + l) {
+          start->base = base;
+          start->s = s;
+          start->tok0 = tok;
+          return true;
+        }
+        base += l;
+        return false;
+      });
   }
-  if (tid == 0) *w.plan = Plan{n_entries, n_split, 0, 0};
+  fence_async_smem();  // the scratch becomes a destination of TMA copies
+  __syncthreads();
 }
 
 // ------------------------------------------------------------------- main kernel
@@ -263,6 +264,8 @@ struct Ctl {
   uint64_t q_full[2], q_empty[2], qc_full[2], kv_full[5], kv_empty[5], raw_full[3], raw_empty[3], s_full[2], p_full[2][2],
       o_done[2], it_full[2], it_empty[2];
   Item item[2];
+  Start start;
+  long long scan[16];
   uint32_t tmem;
   volatile int abort_flag;
   float inv_sig[kE4M3 ? 2 : 1][2][kE4M3 ? kTile : 1];  // [item parity][tile][row]: 1 / Q scale
@@ -273,13 +276,22 @@ constexpr size_t smem_bytes() {
   return 2 * kTileBytes + Cfg<kE4M3>::kStages * kTileBytes + Cfg<kE4M3>::kRaw * kRawBytes +
          sizeof(Ctl<kE4M3>);
 }
+static_assert(kMaxSeqs * sizeof(int) <= Cfg<false>::kStages * kTileBytes &&
+                  kMaxSeqs * sizeof(int) <= Cfg<true>::kStages * kTileBytes + Cfg<true>::kRaw * kRawBytes,
+              "find_start's scratch");
 static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory");
+
+// One 32-byte store (dst 32-byte aligned): whole sectors from a thread that owns a row.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <int kRegs>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Two fp32 at a time (sm_100's packed arithmetic).
 typedef unsigned long long f32x2;
@@ -312,7 +324,8 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
   uint8_t* sraw = skv + C::kStages * kTileBytes;
   Ctl<kE4M3>& ctl = *reinterpret_cast<Ctl<kE4M3>*>(sraw + C::kRaw * kRawBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int* status = p.status != nullptr ? p.status : &w.plan->flags;
+  int* status = p.status != nullptr ? p.status : w.flags;
+  const int g = blockIdx.x % p.Hkv, part = blockIdx.x / p.Hkv;
 
   if (warp == 0) tmem_alloc(&ctl.tmem, 512);
   if (tid == 32) {
@@ -342,8 +355,10 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
-  pdl_wait();  // the plan
   pdl_trigger();
+  int n_parts;
+  find_start<C::kThreads>(p, part, &n_parts, reinterpret_cast<int*>(skv), ctl.scan, &ctl.start);
+  if (part >= n_parts && tid == 0 && g == 0) w.splits[part] = Split{-1, 0, 0, 0};
   volatile int* ab = &ctl.abort_flag;
   const int tok_t = kTile / p.group;  // tokens of one query tile
 
@@ -482,24 +497,42 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
       if (live) {
         if (im.slot < 0) {
           const float f = (l > 0.f ? 1.f / l : 0.f) * (kE4M3 ? __ldg(p.v_scale + im.g) : 1.f);
-          uint4* dst = reinterpret_cast<uint4*>(
-              p.out + (static_cast<size_t>(im.row0 + im.tok0 + tok) * p.Hq + im.g * p.group + row % p.group) * kDh);
+          uint16_t* dst =
+              p.out + (static_cast<size_t>(im.row0 + im.tok0 + tok) * p.Hq + im.g * p.group + row % p.group) * kDh;
+          // out is 16-byte aligned: 32-byte stores where it is 32-byte aligned too
+          const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            uint32_t r[4];
+          for (int i = 0; i < 8; ++i) {
+            uint32_t r[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * i + 2 * j] * f, o[8 * i + 2 * j + 1] * f);
+            for (int j = 0; j < 8; ++j) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(o[16 * i + 2 * j] * f, o[16 * i + 2 * j + 1] * f);
               r[j] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            dst[i] = make_uint4(r[0], r[1], r[2], r[3]);
+            if (wide) {
+              store32(dst + 16 * i, r);
+            } else {
+              reinterpret_cast<uint4*>(dst)[2 * i] = make_uint4(r[0], r[1], r[2], r[3]);
+              reinterpret_cast<uint4*>(dst)[2 * i + 1] = make_uint4(r[4], r[5], r[6], r[7]);
+            }
           }
         } else {
-          const size_t at = (static_cast<size_t>(im.slot) * p.Hkv + im.g) * rows_per_slot + t * kTile + row;
+          const size_t at = static_cast<size_t>(im.slot) * rows_per_slot + t * kTile + row;
           *reinterpret_cast<float2*>(w.ml + at * 2) = make_float2(m == -INFINITY ? -INFINITY : m * c, l);
-          float4* dst = reinterpret_cast<float4*>(w.po + at * kDh);
+          float* dst = w.po + at * kDh;  // 256-byte aligned in a workspace that is 32-byte aligned
+          const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 16; ++i) {
+            uint32_t r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(o[8 * i + j]);
+            if (wide) {
+              store32(dst + 8 * i, r);
+            } else {
+              reinterpret_cast<uint4*>(dst)[2 * i] = make_uint4(r[0], r[1], r[2], r[3]);
+              reinterpret_cast<uint4*>(dst)[2 * i + 1] = make_uint4(r[4], r[5], r[6], r[7]);
+            }
+          }
         }
       }
     }
@@ -594,7 +627,6 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
   } else if (warp == 9) {
     // ================================================================ loader
     regs_dec<kE4M3 ? 64 : 88>();
-    const int n_items = w.plan->n_entries * p.Hkv;
     const int ps = 1 << p.b.page_shift;
     const int box = min(ps, kTile), n_box = kTile / box;
     const int my_box = kE4M3 ? lane : lane >> 1, half = kE4M3 ? 0 : lane & 1;
@@ -604,34 +636,75 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
     uint32_t li = 0, qn[2] = {0, 0};
     constexpr int kRing = kE4M3 ? C::kRaw : C::kStages;
     bool ok = true;
+    // the part [pos, end) of the line; the pair at its first place
+    const int pair = 2 * tok_t;
+    const long long total = ctl.start.total;
+    long long base = ctl.start.base, pos = part < n_parts ? total * part / n_parts : 0,
+              end = part < n_parts ? total * (part + 1) / n_parts : 0;
+    int s = ctl.start.s, tok0 = ctl.start.tok0;
+    bool bad;
+    PagedSeq q{0, 0, 0};
+    const bool deal = ctl.start.deal != 0 && part < n_parts;
+    if (!deal && pos < end) q = chunk_seq(p, s, &bad);
+    Split left{-1, 0, 0, 0};
     for (int it = 0; ok; ++it) {
-      if (!(ok = mma_wait(&ctl.it_empty[it & 1], ((it >> 1) & 1) ^ 1, ab, status))) break;
       Item im{};
-      if (lane == 0) {
-        const int i = atomicAdd(&w.plan->counter, 1);
-        if (i < n_items) {
-          const Entry e = w.entries[i / p.Hkv];
-          bool bad;
-          const PagedSeq q = chunk_seq(p, e.s, &bad);
+      im.end = 1;
+      if (deal) {
+        const int i = ctl.start.n_pairs - 1 - (it * n_parts + ((it & 1) ? n_parts - 1 - part : part));
+        if (i >= 0) {
+          s = 0;
+          for (int x = 1; x < p.b.B; ++x)
+            if (ctl.start.first_pair[x] <= i) s = x;
+          q = chunk_seq(p, s, &bad);
+          tok0 = (i - ctl.start.first_pair[s]) * pair;
+          const Keys k = pair_keys(q, tok0, pair, p.window);
           im.row0 = q.row0;
-          im.tok0 = e.tok0;
-          im.live = min(q.n - e.tok0, 2 * tok_t);
+          im.tok0 = tok0;
+          im.live = min(q.n - tok0, pair);
           im.n = q.n;
           im.kv = q.kv;
-          im.kt0 = e.kt0;
-          im.kt1 = e.kt1;
-          im.g = i % p.Hkv;
-          im.slot = e.slot;
-          im.s = e.s;
+          im.kt0 = k.kt0;
+          im.kt1 = k.kt1;
+          im.g = g;
+          im.slot = -1;
+          im.s = s;
           im.end = 0;
-        } else {
-          im.end = 1;
         }
+      } else if (pos < end) {
+        while (tok0 >= q.n || q.kv <= 0) {  // the next sequence with new tokens
+          q = chunk_seq(p, ++s, &bad);
+          tok0 = 0;
+        }
+        const Keys k = pair_keys(q, tok0, pair, p.window);
+        const int len = k.length();
+        // a boundary within a pair's first kFill places is one in front of it
+        if (pos - base <= kFill) pos = base;
+        if (end > base + kFill) {
+          const bool whole = pos == base && end >= base + len, goes_on = end < base + len;
+          im.row0 = q.row0;
+          im.tok0 = tok0;
+          im.live = min(q.n - tok0, pair);
+          im.n = q.n;
+          im.kv = q.kv;
+          im.kt0 = k.kt0 + (pos == base ? 0 : static_cast<int>(pos - base) - kFill);
+          im.kt1 = goes_on ? k.kt0 + static_cast<int>(end - base) - kFill : k.kt1;
+          im.g = g;
+          im.slot = whole ? -1 : static_cast<int>(slot_of(part, p.Hkv, g, goes_on));
+          im.s = s;
+          im.end = 0;
+          if (goes_on && pos == base)  // ends in the part that holds the pair's last place
+            left = Split{s, tok0, part, static_cast<int>(((base + len) * n_parts - 1) / total)};
+          pos = base += len;
+          tok0 += pair;
+        }
+      }
+      if (!(ok = mma_wait(&ctl.it_empty[it & 1], ((it >> 1) & 1) ^ 1, ab, status))) break;
+      if (lane == 0) {
         ctl.item[it & 1] = im;
         mbar_arrive(&ctl.it_full[it & 1]);
       }
       __syncwarp();
-      im = ctl.item[it & 1];
       if (im.end) break;
       const int nt = im.live > tok_t ? 2 : 1;
       for (int t = 0; t < nt && ok; ++t) {
@@ -678,6 +751,7 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
         r = nxt;
       }
     }
+    if (lane == 0 && g == 0 && part < n_parts) w.splits[part] = left;
     // copies in flight land before the CTA ends (only after a wait gave up)
     if (!ok) {
       const long long t0 = clock64();
@@ -760,58 +834,77 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// One warp per query row of a split entry: joins its pieces in key order. The
-// same grid writes zeros for the tokens of invalid sequences.
+// Joins the pieces of the pairs that parts cut, in key order: a CTA takes 32
+// rows of the pair that one part left unfinished in one kv head, a warp four of
+// them at once. The last CTA writes zeros for the tokens of invalid sequences.
 constexpr int kCombineThreads = 256;
+constexpr int kCombineRows = 4 * kCombineThreads / 32;
 
 __global__ void __launch_bounds__(kCombineThreads) k_chunk_combine(PagedAttnParams p, Ws w, int rows_per_slot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long warps = static_cast<long long>(gridDim.x) * (kCombineThreads / 32);
-  const long long me = static_cast<long long>(blockIdx.x) * (kCombineThreads / 32) + (threadIdx.x >> 5);
-  const int tok_t = kTile / p.group;
-  const long long n = static_cast<long long>(__ldcg(&w.plan->n_split)) * p.Hkv * rows_per_slot;
-  for (long long i = me; i < n; i += warps) {
-    const int r = static_cast<int>(i % rows_per_slot);
-    const long long x = i / rows_per_slot;
-    const int g = static_cast<int>(x % p.Hkv);
-    const int4 sv = __ldcg(reinterpret_cast<const int4*>(w.splits + x / p.Hkv));
-    const Split sp{sv.x, sv.y, sv.z, sv.w};
-    bool bad;
-    const PagedSeq q = chunk_seq(p, sp.s, &bad);
-    const int rt = r % kTile, tok = sp.tok0 + (r / kTile) * tok_t + rt / p.group;
-    if (rt >= tok_t * p.group || tok >= q.n) continue;
-    float M = -INFINITY;
-    for (int k = lane; k < sp.parts; k += 32)
-      M = fmaxf(M, __ldcg(w.ml + ((static_cast<size_t>(sp.slot + k) * p.Hkv + g) * rows_per_slot + r) * 2));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < sp.parts; ++k) {
-      const size_t at = (static_cast<size_t>(sp.slot + k) * p.Hkv + g) * rows_per_slot + r;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(w.ml + at * 2));
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(w.po + at * kDh) + lane);
-      const float f = ml.x == -INFINITY ? 0.f : exp2_ftz(ml.x - M);
-      l = fmaf(ml.y, f, l);
-      acc.x = fmaf(o.x, f, acc.x);
-      acc.y = fmaf(o.y, f, acc.y);
-      acc.z = fmaf(o.z, f, acc.z);
-      acc.w = fmaf(o.w, f, acc.w);
+  if (blockIdx.x + 1 == gridDim.x) {
+    for (int s = warp; s < p.b.B; s += kCombineThreads / 32) {
+      bool bad;
+      const PagedSeq q = chunk_seq(p, s, &bad);
+      if (q.n <= 0 || q.kv > 0) continue;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<size_t>(q.row0) * p.Hq * kDh);
+      const long long m = static_cast<long long>(q.n) * p.Hq * (kDh / 8);
+      for (long long i = lane; i < m; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
     }
-    const float f = (l > 0.f ? 1.f / l : 0.f) * (p.v_scale != nullptr ? __ldg(p.v_scale + g) : 1.f);
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * f, acc.y * f), b = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+    return;
+  }
+  const int blocks = rows_per_slot / kCombineRows;
+  const int x = blockIdx.x / blocks, part = x / p.Hkv, g = x - part * p.Hkv;
+  const int4 sv = __ldcg(reinterpret_cast<const int4*>(w.splits + part));
+  if (sv.x < 0) return;
+  const Split sp{sv.x, sv.y, sv.z, sv.w};
+  const int tok_t = kTile / p.group;
+  bool bad;
+  const PagedSeq q = chunk_seq(p, sp.s, &bad);
+  const int r0 = (blockIdx.x - x * blocks) * kCombineRows + 4 * warp;
+  float M[4], l[4];
+  float4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    M[i] = -INFINITY;
+    l[i] = 0.f;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 2
+  for (int k = sp.first; k <= sp.last; ++k) {
+    const size_t at = slot_of(k, p.Hkv, g, k < sp.last) * rows_per_slot + r0;
+    float2 ml[4];
+    float4 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ml[i] = __ldcg(reinterpret_cast<const float2*>(w.ml + (at + i) * 2));
+      o[i] = __ldcg(reinterpret_cast<const float4*>(w.po + (at + i) * kDh) + lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // rows past the pair's tokens were not written: what is read for them is dropped below
+      if (!(ml[i].x > -INFINITY)) continue;
+      const float mx = fmaxf(M[i], ml[i].x);
+      const float f0 = M[i] == -INFINITY ? 0.f : exp2_ftz(M[i] - mx), f1 = exp2_ftz(ml[i].x - mx);
+      M[i] = mx;
+      l[i] = fmaf(l[i], f0, ml[i].y * f1);
+      acc[i].x = fmaf(acc[i].x, f0, o[i].x * f1);
+      acc[i].y = fmaf(acc[i].y, f0, o[i].y * f1);
+      acc[i].z = fmaf(acc[i].z, f0, o[i].z * f1);
+      acc[i].w = fmaf(acc[i].w, f0, o[i].w * f1);
+    }
+  }
+  const float vs = p.v_scale != nullptr ? __ldg(p.v_scale + g) : 1.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i, rt = r % kTile, tok = sp.tok0 + (r / kTile) * tok_t + rt / p.group;
+    if (rt >= tok_t * p.group || tok >= q.n) continue;
+    const float f = (l[i] > 0.f ? 1.f / l[i] : 0.f) * vs;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[i].x * f, acc[i].y * f),
+                         b = __floats2bfloat162_rn(acc[i].z * f, acc[i].w * f);
     reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(q.row0 + tok) * p.Hq + g * p.group + rt % p.group) * kDh)[lane] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-  for (long long s = me; s < p.b.B; s += warps) {
-    bool bad;
-    const PagedSeq q = chunk_seq(p, static_cast<int>(s), &bad);
-    if (q.n <= 0 || q.kv > 0) continue;
-    uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<size_t>(q.row0) * p.Hq * kDh);
-    const long long m = static_cast<long long>(q.n) * p.Hq * (kDh / 8);
-    for (long long i = lane; i < m; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -833,17 +926,16 @@ cudaError_t launch_pdl(void (*kern)(Args...), int grid, int block, size_t smem, 
 
 }  // namespace
 
-size_t paged_chunk_workspace(int T, int B, int n_q_heads, int n_kv_heads, int max_q) {
+size_t paged_chunk_workspace(int n_q_heads, int n_kv_heads, int max_q) {
   Ws w;
-  const int group = n_q_heads / n_kv_heads;
-  return carve(&w, nullptr, T, B, n_kv_heads, group, slot_rows(max_q, group));
+  return carve(&w, nullptr, n_kv_heads, slot_rows(max_q, n_q_heads / n_kv_heads));
 }
 
 int paged_chunk_launch(const PagedAttnParams& p, int cache_dtype, size_t ws_bytes, cudaStream_t st) {
   const bool e4m3 = cache_dtype == FLINT_KV_E4M3;
   const int rows = slot_rows(p.max_q, p.group);
   Ws w;
-  const size_t need = carve(&w, p.ws, p.b.T, p.b.B, p.Hkv, p.group, rows);
+  const size_t need = carve(&w, p.ws, p.Hkv, rows);
   if (p.ws == nullptr || ws_bytes < need)
     return flint_fail_external(FLINT_ERR_WORKSPACE, "flint_paged_attention: workspace too small");
   CUtensorMap mq, mk, mv;
@@ -871,13 +963,14 @@ int paged_chunk_launch(const PagedAttnParams& p, int cache_dtype, size_t ws_byte
                           : reinterpret_cast<const void*>(k_paged_chunk<false>);
   cudaError_t e = flint_ensure_smem(kern);
   if (e != cudaSuccess) return flint_fail_external(FLINT_ERR_CUDA, cudaGetErrorString(e));
-  k_chunk_plan<<<1, kPlanThreads, 0, st>>>(p, w);
+  const int grid = parts_per_head(p.Hkv) * p.Hkv;
+  if (e4m3)
+    k_paged_chunk<true><<<grid, Cfg<true>::kThreads, smem_bytes<true>(), st>>>(mq, mk, mv, p, w, rows);
+  else
+    k_paged_chunk<false><<<grid, Cfg<false>::kThreads, smem_bytes<false>(), st>>>(mq, mk, mv, p, w, rows);
   e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = e4m3 ? launch_pdl(k_paged_chunk<true>, kCtas, Cfg<true>::kThreads, smem_bytes<true>(), st, mq, mk, mv, p, w, rows)
-             : launch_pdl(k_paged_chunk<false>, kCtas, Cfg<false>::kThreads, smem_bytes<false>(), st, mq, mk, mv, p, w,
-                          rows);
-  if (e == cudaSuccess) e = launch_pdl(k_chunk_combine, 2 * kCtas, kCombineThreads, 0, st, p, w, rows);
+    e = launch_pdl(k_chunk_combine, grid * (rows / kCombineRows) + 1, kCombineThreads, 0, st, p, w, rows);
   if (e != cudaSuccess) return flint_fail_external(FLINT_ERR_CUDA, cudaGetErrorString(e));
   return FLINT_OK;
 }

@@ -172,6 +172,32 @@ def test_chunk_peaked_scores():
         R.check_attention(R.run_attention(b), b, what=f"peaked, e4m3 {e4m3}")
 
 
+@pytest.mark.parametrize("B,seed", [(1, 1), (40, 2), (200, 3)])
+def test_chunk_many_sequences(B, seed):
+    # parts that begin and end in every place of the line, sequences without tokens between
+    g = torch.Generator().manual_seed(seed)
+    new = [int(x) for x in torch.randint(0, 30 if B > 1 else 900, (B,), generator=g)]
+    new[0] = max(new[0], 18)  # more than one register tile: the chunk kernel
+    kv = [n + int(x) for n, x in zip(new, torch.randint(0, 300, (B,), generator=g))]
+    b = R.Paged(seed, new, kv, 2, 2, 16)
+    R.check_attention(R.run_attention(b), b, what=f"{B} sequences")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunk_pairs_dealt_whole(e4m3):
+    # many short pairs a CTA (150 kv heads: one CTA each), sequences without tokens between
+    b = R.Paged(5, [300, 0, 70, 1, 0, 33], [310, 4, 90, 30, 0, 33], 150, 150, 16, e4m3)
+    R.check_attention(R.run_attention(b), b, what="whole pairs")
+    b = R.Paged(6, [1500], [1500], 74, 74, 64, e4m3)
+    R.check_attention(R.run_attention(b), b, what="one prompt")
+
+
+def test_chunk_more_kv_heads_than_parts():
+    for hq, hkv in ((150, 150), (160, 80)):
+        b = R.Paged(hq, [20, 17], [20, 150], hq, hkv, 16)
+        R.check_attention(R.run_attention(b), b, what=f"{hq}/{hkv}")
+
+
 def test_chunk_split_over_keys():
     # one short piece of a long sequence: its key tiles go to many CTAs and are joined
     for e4m3 in (False, True):

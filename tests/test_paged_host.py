@@ -66,7 +66,7 @@ def test_attention_arguments(L):
     assert _attn(L, hq=34, hkv=2) == -2       # 17 query heads per kv head
     assert _attn(L, hq=30) == -2
     assert _attn(L, hq=2048, hkv=128) == -2
-    assert _attn(L, B=65536) == -2
+    assert _attn(L, B=32769) == -2
     assert _attn(L, max_q=0) == -1
     assert _attn(L, pages=0) == -1
     assert _attn(L, window=-1) == -1
