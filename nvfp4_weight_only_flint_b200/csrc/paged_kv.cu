@@ -9,10 +9,16 @@
 //   (y_i, y_{i+64}) turned by the angle row of the token's position
 //   q_out = bf16(y); K row = bf16(y) or E4M3(y / k_scale); V row likewise from x
 //
-// One half-warp takes kHeads consecutive heads of one token: lane l holds
-// elements 8l .. 8l+7 of each (a 16-byte load; all heads' loads are issued
-// before the first is used), so the cos/sin row, the page lookup and the
-// search for the token's sequence are done once for kHeads heads.
+// One half-warp takes kHeads consecutive heads of one token; lane l holds
+// elements 4l .. 4l + 3 and their rotation partners 64 + 4l .. 64 + 4l + 3 of
+// each (two 8-byte loads, a half-warp reading two 128-byte runs; all heads'
+// loads are issued before the first is used), so no element changes lanes, and
+// the angles, the page lookup and the search for the token's sequence are done
+// once for kHeads heads. Partners in other lanes, four heads a half-warp and
+// IEEE root and quotients took 41 us for 7,803 tokens against 34.6, bound by
+// instruction issue; what is left is the latency of the lookups in front of the
+// angles (4.65 TB/s; 3, 5 or 8 heads a half-warp 36, 35 and 38 us). Calls of few
+// tokens take two heads a half-warp: 64 tokens 3.1 us against 4.0.
 // HBM-bound: (Hq + 2 Hkv) 256 bytes read and Hq 256 + 2 Hkv 128 e written per
 // token (e = 2 or 1 bytes), the cos/sin row (512 bytes) once per position.
 #include "paged.cuh"
@@ -20,7 +26,6 @@
 namespace flint {
 namespace {
 
-constexpr int kHeads = 4;
 constexpr int kThreads = 128;
 constexpr int kUnitsPerCta = kThreads / 16;
 
@@ -47,7 +52,7 @@ struct AppendParams {
   float eps;
 };
 
-template <bool kE4M3>
+template <bool kE4M3, int kHeads>
 __global__ void __launch_bounds__(kThreads) k_paged_append(AppendParams p) {
   const int lane = threadIdx.x & 15;
   const unsigned hmask = 0xFFFFu << (threadIdx.x & 16);
@@ -57,16 +62,14 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(AppendParams p) {
   const int h0 = static_cast<int>(unit - static_cast<unsigned>(t) * p.units) * kHeads;
   const int H = p.Hq + 2 * p.Hkv;
   const int nh = min(kHeads, H - h0);
-  uint4 raw[kHeads];
-  const uint4* src = reinterpret_cast<const uint4*>(p.qkv + (static_cast<size_t>(t) * H + h0) * kPagedHeadDim) + lane;
+  uint2 raw[kHeads][2];
+  const uint2* src = reinterpret_cast<const uint2*>(p.qkv + (static_cast<size_t>(t) * H + h0) * kPagedHeadDim) + lane;
 #pragma unroll
   for (int i = 0; i < kHeads; ++i)
-    if (i < nh) raw[i] = __ldcs(src + i * 16);
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (p.q_w != nullptr) {
-    wq = __ldg(reinterpret_cast<const uint4*>(p.q_w) + lane);
-    wk = __ldg(reinterpret_cast<const uint4*>(p.k_w) + lane);
-  }
+    if (i < nh) {
+      raw[i][0] = __ldcs(src + i * 32);
+      raw[i][1] = __ldcs(src + i * 32 + 16);
+    }
   // the token's sequence: the last s in [0, B) with q_start[s] <= t, by a
   // search of 16 probes a step (the half-warp's lanes)
   int lo = -1, hi = p.b.B + 1;  // q_start[lo] <= t < q_start[hi] in sorted data
@@ -92,61 +95,56 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(AppendParams p) {
   }
   const bool turn = p.rope && placed && pos < p.max_pos;
   if (lane == 0 && p.status != nullptr && (slot < 0 || (p.rope && !turn))) atomicOr(p.status, FLINT_DEVCHECK_INDEX);
-  // angles of pairs (c, c + 64): lanes 0..7 hold the first halves, 8..15 the second
-  float cc[8], sn[8];
+  // angles of this lane's four pairs (c, c + 64)
+  float cc[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
   if (turn) {
-    const float* row = p.cos_sin + static_cast<size_t>(pos) * kPagedHeadDim + 8 * (lane & 7);
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(row)), c1 = __ldg(reinterpret_cast<const float4*>(row + 4));
-    const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + 64)), s1 = __ldg(reinterpret_cast<const float4*>(row + 68));
-    cc[0] = c0.x; cc[1] = c0.y; cc[2] = c0.z; cc[3] = c0.w;
-    cc[4] = c1.x; cc[5] = c1.y; cc[6] = c1.z; cc[7] = c1.w;
-    sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
-    sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
-    // second halves turn with + partner sin, first halves with - partner sin
-    if (lane < 8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sn[j] = -sn[j];
-    }
+    const float4* row = reinterpret_cast<const float4*>(p.cos_sin + static_cast<size_t>(pos) * kPagedHeadDim) + lane;
+    const float4 c = __ldg(row), s = __ldg(row + 16);
+    cc[0] = c.x; cc[1] = c.y; cc[2] = c.z; cc[3] = c.w;
+    sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
   }
+  // weights of the query heads, then of the key heads, by this lane's elements
+  float w[8];
+  int w_of = -1;  // 0: w holds the queries' weights, 1: the keys'
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
     if (i >= nh) break;
     const int h = h0 + i;
-    const uint32_t rw[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    float y[8];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      y[2 * q] = bf_lo(rw[q]);
-      y[2 * q + 1] = bf_hi(rw[q]);
-    }
     const bool is_v = h >= p.Hq + p.Hkv;
+    float y[8] = {bf_lo(raw[i][0].x), bf_hi(raw[i][0].x), bf_lo(raw[i][0].y), bf_hi(raw[i][0].y),
+                  bf_lo(raw[i][1].x), bf_hi(raw[i][1].x), bf_lo(raw[i][1].y), bf_hi(raw[i][1].y)};
     if (!is_v) {
       if (p.q_w != nullptr) {
-        const uint4 w4 = h < p.Hq ? wq : wk;
-        const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
+        if (w_of != (h >= p.Hq)) {
+          w_of = h >= p.Hq;
+          const uint2* wp = reinterpret_cast<const uint2*>(w_of ? p.k_w : p.q_w) + lane;
+          const uint2 w0 = __ldg(wp), w1 = __ldg(wp + 16);
+          w[0] = bf_lo(w0.x); w[1] = bf_hi(w0.x); w[2] = bf_lo(w0.y); w[3] = bf_hi(w0.y);
+          w[4] = bf_lo(w1.x); w[5] = bf_hi(w1.x); w[6] = bf_lo(w1.y); w[7] = bf_hi(w1.y);
+        }
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(hmask, ss, o);
-        const float r = 1.f / sqrtf(ss / static_cast<float>(kPagedHeadDim) + p.eps);
+        // rsqrtf: within 2 ulp of the root's reciprocal
+        const float r = rsqrtf(fmaf(ss, 1.f / kPagedHeadDim, p.eps));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          y[2 * q] = y[2 * q] * r * bf_lo(ww[q]);
-          y[2 * q + 1] = y[2 * q + 1] * r * bf_hi(ww[q]);
-        }
+        for (int j = 0; j < 8; ++j) y[j] *= r * w[j];
       }
       if (turn) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float partner = __shfl_xor_sync(hmask, y[j], 8);
-          y[j] = fmaf(y[j], cc[j], partner * sn[j]);
+        for (int j = 0; j < 4; ++j) {
+          const float a = y[j], b = y[4 + j];
+          y[j] = fmaf(a, cc[j], -b * sn[j]);
+          y[4 + j] = fmaf(b, cc[j], a * sn[j]);
         }
       }
     }
     if (h < p.Hq) {
-      uint4* dst = reinterpret_cast<uint4*>(p.q_out + (static_cast<size_t>(t) * p.Hq + h) * kPagedHeadDim);
-      dst[lane] = make_uint4(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]), pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
+      uint2* dst = reinterpret_cast<uint2*>(p.q_out + (static_cast<size_t>(t) * p.Hq + h) * kPagedHeadDim) + lane;
+      dst[0] = make_uint2(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]));
+      dst[16] = make_uint2(pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
       continue;
     }
     if (slot < 0) continue;
@@ -154,17 +152,18 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(AppendParams p) {
     const size_t at = (static_cast<size_t>(slot) * p.Hkv + g) * kPagedHeadDim;
     void* pool = is_v ? p.v_cache : p.k_cache;
     if constexpr (kE4M3) {
-      // one rounding, from fp32: the quotient is not rounded to bf16 first
-      const float sc = __ldg((is_v ? p.v_scale : p.k_scale) + g);
+      // one rounding, from fp32: the quotient (by a reciprocal, within 2 ulp) is not rounded to bf16 first
+      const float inv = 1.f / __ldg((is_v ? p.v_scale : p.k_scale) + g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = y[j] / sc;
-      const uint2 o = make_uint2(pack_e4m3x2(y[0], y[1]) | (pack_e4m3x2(y[2], y[3]) << 16),
-                                 pack_e4m3x2(y[4], y[5]) | (pack_e4m3x2(y[6], y[7]) << 16));
-      reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at)[lane] = o;
+      for (int j = 0; j < 8; ++j) y[j] *= inv;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(pool) + at) + lane;
+      dst[0] = pack_e4m3x2(y[0], y[1]) | (pack_e4m3x2(y[2], y[3]) << 16);
+      dst[16] = pack_e4m3x2(y[4], y[5]) | (pack_e4m3x2(y[6], y[7]) << 16);
     } else {
       // values are copied bit for bit
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at)[lane] =
-          is_v ? raw[i] : make_uint4(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]), pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(pool) + at) + lane;
+      dst[0] = is_v ? raw[i][0] : make_uint2(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]));
+      dst[16] = is_v ? raw[i][1] : make_uint2(pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
     }
   }
 }
@@ -212,15 +211,16 @@ extern "C" int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32
   p.max_pos = max_pos;
   p.rope = rope ? 1 : 0;
   p.eps = eps;
-  p.units = (n_q_heads + 2 * n_kv_heads + kHeads - 1) / kHeads;
+  const int heads = T <= 512 ? 2 : 4;
+  p.units = (n_q_heads + 2 * n_kv_heads + heads - 1) / heads;
   // units are counted in 32 bits
   const long long blocks = (static_cast<long long>(T) * p.units + kUnitsPerCta - 1) / kUnitsPerCta;
   if (blocks > 0x7fffffffLL / kUnitsPerCta) return flint_fail_external(FLINT_ERR_UNSUPPORTED_SHAPE, "too many tokens");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache_dtype == FLINT_KV_E4M3)
-    k_paged_append<true><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
-  else
-    k_paged_append<false><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
+  const bool e4m3 = cache_dtype == FLINT_KV_E4M3;
+  auto kern = heads == 2 ? (e4m3 ? k_paged_append<true, 2> : k_paged_append<false, 2>)
+                         : (e4m3 ? k_paged_append<true, 4> : k_paged_append<false, 4>);
+  kern<<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return flint_fail_external(FLINT_ERR_CUDA, cudaGetErrorString(e));
   return FLINT_OK;

@@ -105,6 +105,16 @@ def test_append_finds_the_sequence(B, T):
     _check(b, _run(b, qw, kw, cs, True), qw, kw, cs, True)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T", [511, 512, 513])
+def test_append_call_sizes(T, e4m3):
+    # two heads a half-warp up to 512 tokens, four above
+    b = R.Paged(T, [T - 40, 40], [T, 77], 6, 1, 64, e4m3)
+    cs = _angles(T)
+    qw, kw = _weights(5)
+    _check(b, _run(b, qw, kw, cs, True), qw, kw, cs, True)
+
+
 def test_append_saturates_e4m3_and_large_values():
     b = R.Paged(5, [4], [4], 4, 2, 16, e4m3=True)
     b.qkv = b.qkv * 3000
