@@ -40,7 +40,7 @@ constexpr int kDh = kPagedHeadDim;
 constexpr int kWarps = 4;
 constexpr int kBlock = 16;
 constexpr int kQuantum = kWarps * kBlock;
-constexpr int kCtaSlots = 2 * 148;
+constexpr int kCtaSlots = 2 * 148;  // two CTAs per SM (three of an E4M3 cache, 168 registers and four stages: 61 us against 58)
 constexpr int kRowsMax = kDecodeRows;
 
 template <bool kE4M3>
@@ -339,11 +339,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
       }
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[16][kTall ? 4 : 2];
+    // rows 8 .. 15 of a low tile stay zero (their weights are): the accumulators
+    // of both halves are kept all the same, so that none has to be cleared
+    float o[16][4];
 #pragma unroll
     for (int j = 0; j < 16; ++j)
 #pragma unroll
-      for (int c = 0; c < (kTall ? 4 : 2); ++c) o[j][c] = 0.f;
+      for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
 
     for (int b = 0; b < n_blocks; ++b) {
       if (b + R::kStages - 1 < n_blocks) load_block(b + R::kStages - 1);
@@ -352,7 +354,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
       __syncwarp();
       const uint32_t kr = ring + (b % R::kStages) * stage_bytes<kE4M3>();
       const uint32_t vr = kr + kBlock * R::kRowBytes;
+      // two accumulators a column tile: shorter chains
       float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+      float u0[4] = {0.f, 0.f, 0.f, 0.f}, u1[4] = {0.f, 0.f, 0.f, 0.f};
       if constexpr (kE4M3) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -362,8 +366,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            mma16<true>(s0, qa[4 * half + w], e4m3x2_to_f16x2(wa[w]), e4m3x2_to_f16x2(wa[w] >> 16));
-            mma16<true>(s1, qa[4 * half + w], e4m3x2_to_f16x2(wc[w]), e4m3x2_to_f16x2(wc[w] >> 16));
+            mma16<true>(w & 1 ? u0 : s0, qa[4 * half + w], e4m3x2_to_f16x2(wa[w]), e4m3x2_to_f16x2(wa[w] >> 16));
+            mma16<true>(w & 1 ? u1 : s1, qa[4 * half + w], e4m3x2_to_f16x2(wc[w]), e4m3x2_to_f16x2(wc[w] >> 16));
           }
         }
       } else {
@@ -372,15 +376,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
         for (int ks = 0; ks < 8; ++ks) {
           uint32_t b00, b01, b10, b11;
           ldsm4(kr + mr * R::kRowBytes + 32 * ks + mc, b00, b01, b10, b11);
-          mma16<false>(s0, qa[ks], b00, b01);
-          mma16<false>(s1, qa[ks], b10, b11);
+          mma16<false>(ks & 1 ? u0 : s0, qa[ks], b00, b01);
+          mma16<false>(ks & 1 ? u1 : s1, qa[ks], b10, b11);
         }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s0[c] += u0[c];
+        s1[c] += u1[c];
       }
       // this lane: keys 2 t4, 2 t4 + 1 (s0) and 8 + 2 t4, 9 + 2 t4 (s1) of rows gq (c 0, 1), gq + 8 (c 2, 3)
       const int kb = w0 + b * kBlock;
       const bool edge = kb + kBlock > min(w1, kv - n + 1) || (p.window > 0 && kb < kv - p.window);
       uint32_t pa[4] = {0u, 0u, 0u, 0u};
-      float alpha[2];
+      float alpha[2] = {1.f, 1.f};
 #pragma unroll
       for (int x = 0; x < (kTall ? 2 : 1); ++x) {
         float v[4] = {s0[2 * x] * sc[x], s0[2 * x + 1] * sc[x], s1[2 * x] * sc[x], s1[2 * x + 1] * sc[x]};
@@ -418,20 +427,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
         ps += __shfl_xor_sync(0xffffffffu, ps, 2);
         l[x] = fmaf(l[x], alpha[x], ps);
       }
-      auto pv = [&](int j, uint32_t b0, uint32_t b1) {
-        float c[4] = {o[j][0] * alpha[0], o[j][1] * alpha[0], 0.f, 0.f};
-        if constexpr (kTall) {
-          c[2] = o[j][2] * alpha[1];
-          c[3] = o[j][3] * alpha[1];
+      // the maxima rarely move after the first blocks
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          o[j][0] *= alpha[0];
+          o[j][1] *= alpha[0];
+          if constexpr (kTall) {
+            o[j][2] *= alpha[1];
+            o[j][3] *= alpha[1];
+          }
         }
-        mma16<kE4M3>(c, pa, b0, b1);
-        o[j][0] = c[0];
-        o[j][1] = c[1];
-        if constexpr (kTall) {
-          o[j][2] = c[2];
-          o[j][3] = c[3];
-        }
-      };
+      }
+      auto pv = [&](int j, uint32_t b0, uint32_t b1) { mma16<kE4M3>(o[j], pa, b0, b1); };
       if constexpr (kE4M3) {
         // codes 16 gq .. 16 gq + 15 of keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4:
         // MMA column gq of tile j is dimension 16 gq + j
