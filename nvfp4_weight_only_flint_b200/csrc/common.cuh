@@ -8,6 +8,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "flint_moe.h"
 
 namespace flint {
@@ -107,6 +109,24 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launches a kernel that may be scheduled while its predecessor in the stream
+// drains; the kernel calls pdl_wait before it touches global memory.
+template <typename... Args>
+inline cudaError_t launch_pdl(void (*kern)(Args...), dim3 grid, int block, size_t smem, cudaStream_t st,
+                              const std::common_type_t<Args>&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 __device__ __forceinline__ uint4 lds128(const void* p) {

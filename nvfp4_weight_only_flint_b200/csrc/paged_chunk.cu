@@ -38,8 +38,6 @@
 // shared memory, so whatever unused cache rows hold stays out of the sums.
 #include <cuda.h>
 
-#include <type_traits>
-
 #include "paged_attn.cuh"
 #include "tcgen05.cuh"
 
@@ -355,6 +353,7 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
+  pdl_wait();
   pdl_trigger();
   int n_parts;
   find_start<C::kThreads>(p, part, &n_parts, reinterpret_cast<int*>(skv), ctl.scan, &ctl.start);
@@ -843,6 +842,7 @@ constexpr int kCombineRows = 4 * kCombineThreads / 32;
 __global__ void __launch_bounds__(kCombineThreads) k_chunk_combine(PagedAttnParams p, Ws w, int rows_per_slot) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
+  pdl_trigger();
   if (blockIdx.x + 1 == gridDim.x) {
     for (int s = warp; s < p.b.B; s += kCombineThreads / 32) {
       bool bad;
@@ -908,22 +908,6 @@ __global__ void __launch_bounds__(kCombineThreads) k_chunk_combine(PagedAttnPara
   }
 }
 
-template <typename... Args>
-cudaError_t launch_pdl(void (*kern)(Args...), int grid, int block, size_t smem, cudaStream_t st,
-                       const std::common_type_t<Args>&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 }  // namespace
 
 size_t paged_chunk_workspace(int n_q_heads, int n_kv_heads, int max_q) {
@@ -964,11 +948,9 @@ int paged_chunk_launch(const PagedAttnParams& p, int cache_dtype, size_t ws_byte
   cudaError_t e = flint_ensure_smem(kern);
   if (e != cudaSuccess) return flint_fail_external(FLINT_ERR_CUDA, cudaGetErrorString(e));
   const int grid = parts_per_head(p.Hkv) * p.Hkv;
-  if (e4m3)
-    k_paged_chunk<true><<<grid, Cfg<true>::kThreads, smem_bytes<true>(), st>>>(mq, mk, mv, p, w, rows);
-  else
-    k_paged_chunk<false><<<grid, Cfg<false>::kThreads, smem_bytes<false>(), st>>>(mq, mk, mv, p, w, rows);
-  e = cudaGetLastError();
+  e = e4m3 ? launch_pdl(k_paged_chunk<true>, grid, Cfg<true>::kThreads, smem_bytes<true>(), st, mq, mk, mv, p, w, rows)
+           : launch_pdl(k_paged_chunk<false>, grid, Cfg<false>::kThreads, smem_bytes<false>(), st, mq, mk, mv, p, w,
+                        rows);
   if (e == cudaSuccess)
     e = launch_pdl(k_chunk_combine, grid * (rows / kCombineRows) + 1, kCombineThreads, 0, st, p, w, rows);
   if (e != cudaSuccess) return flint_fail_external(FLINT_ERR_CUDA, cudaGetErrorString(e));

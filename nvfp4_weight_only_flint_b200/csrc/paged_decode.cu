@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.x % p.Hkv, part = blockIdx.x / p.Hkv;
   const Ws ws = carve(p.ws, p.b.B, p.Hkv);
+  pdl_wait();
   pdl_trigger();
 
   // ---- the line: thread j sums a run of sequences, the block scans the sums
@@ -587,8 +588,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32) k_paged_combine(PagedAttnP
   const int s = blockIdx.x / per_seq, x = blockIdx.x - s * per_seq;
   const int g = kByRow ? x : x / p.group;
   const Ws ws = carve(p.ws, p.b.B, p.Hkv);
-  const Line ln = line_of(p, s, false);
   pdl_wait();
+  pdl_trigger();
+  const Line ln = line_of(p, s, false);
   const long long base = __ldcg(ws.pre + s), W = __ldcg(ws.pre + p.b.B);
   if (ln.sq.n <= 0) return;
   if (ln.quanta == 0) {
@@ -651,8 +653,7 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   auto kern = k_paged_decode<kE4M3, kTall>;
   cudaError_t e = flint_ensure_smem(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return e;
-  kern<<<ctas_per_head(p.Hkv) * p.Hkv, kWarps * 32, kWarps * ring_bytes<kE4M3>(), st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(kern, ctas_per_head(p.Hkv) * p.Hkv, kWarps * 32, kWarps * ring_bytes<kE4M3>(), st, p);
 }
 
 }  // namespace
@@ -670,17 +671,9 @@ int paged_decode_launch(const PagedAttnParams& p, int cache_dtype, size_t ws_byt
   cudaError_t e = cache_dtype == FLINT_KV_E4M3 ? (tall ? launch<true, true>(p, st) : launch<true, false>(p, st))
                                                : (tall ? launch<false, true>(p, st) : launch<false, false>(p, st));
   if (e != cudaSuccess) return flint_fail_external(FLINT_ERR_CUDA, cudaGetErrorString(e));
-  cudaLaunchConfig_t cfg{};
   const bool by_row = static_cast<long long>(p.Hkv) * p.b.B >= 128;
-  cfg.gridDim = dim3(static_cast<unsigned>(by_row ? p.Hkv : p.Hq) * static_cast<unsigned>(p.b.B));
-  cfg.blockDim = dim3(kCombineWarps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = by_row ? cudaLaunchKernelEx(&cfg, k_paged_combine<true>, p) : cudaLaunchKernelEx(&cfg, k_paged_combine<false>, p);
+  e = by_row ? launch_pdl(k_paged_combine<true>, static_cast<unsigned>(p.Hkv) * p.b.B, kCombineWarps * 32, 0, st, p)
+             : launch_pdl(k_paged_combine<false>, static_cast<unsigned>(p.Hq) * p.b.B, kCombineWarps * 32, 0, st, p);
   if (e != cudaSuccess) return flint_fail_external(FLINT_ERR_CUDA, cudaGetErrorString(e));
   return FLINT_OK;
 }

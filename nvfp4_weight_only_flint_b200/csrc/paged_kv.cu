@@ -54,6 +54,8 @@ struct AppendParams {
 
 template <bool kE4M3, int kHeads>
 __global__ void __launch_bounds__(kThreads) k_paged_append(AppendParams p) {
+  pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 15;
   const unsigned hmask = 0xFFFFu << (threadIdx.x & 16);
   const unsigned unit = blockIdx.x * kUnitsPerCta + (threadIdx.x >> 4);
@@ -220,8 +222,7 @@ extern "C" int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32
   const bool e4m3 = cache_dtype == FLINT_KV_E4M3;
   auto kern = heads == 2 ? (e4m3 ? k_paged_append<true, 2> : k_paged_append<false, 2>)
                          : (e4m3 ? k_paged_append<true, 4> : k_paged_append<false, 4>);
-  kern<<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(kern, static_cast<unsigned>(blocks), kThreads, 0, st, p);
   if (e != cudaSuccess) return flint_fail_external(FLINT_ERR_CUDA, cudaGetErrorString(e));
   return FLINT_OK;
 }
