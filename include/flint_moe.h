@@ -450,7 +450,8 @@ int flint_decode_attention(const uint16_t* q, const uint16_t* k_cache, const uin
  *             position kv_len[s] - n_s + i.
  *   block_table  device int32 [B][max_pages]: position p lives in page
  *             block_table[s][p / page_size], row p % page_size. Entries past
- *             the last used page are not read.
+ *             the last used page are not read, nor are those of pages wholly
+ *             in front of the window of every new token.
  *   k_cache, v_cache  device pools [n_pages][page_size][n_kv_heads][128] of
  *             cache_dtype (flint_kv_dtype); page_size a power of two in
  *             16..1024, n_pages * page_size < 2^31.

@@ -21,6 +21,7 @@
 
 #include <cmath>
 #include <cstdio>
+#include <exception>
 
 #include "flint_moe.h"
 
@@ -134,6 +135,23 @@ PyObject* finish(int rc) {
   Py_RETURN_NONE;
 }
 
+// Torch's checks throw (a sparse tensor has no strides, say); nothing may leave a C function.
+template <PyObject* (*kCall)(PyObject* const*)>
+PyObject* guarded(PyObject*, PyObject* const* v, Py_ssize_t n, Py_ssize_t want) {
+  if (n != want) {
+    PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
+    return nullptr;
+  }
+  try {
+    return kCall(v);
+  } catch (const std::exception& e) {
+    raise(FLINT_ERR_INVALID_ARG, e.what());
+  } catch (...) {
+    raise(FLINT_ERR_INVALID_ARG, "unknown exception");
+  }
+  return nullptr;
+}
+
 // a * b * ..., for sizes; negative factors are left to the C call's checks
 int64_t mul(int64_t a, int64_t b) {
   if (a <= 0 || b <= 0) return 0;
@@ -141,22 +159,9 @@ int64_t mul(int64_t a, int64_t b) {
   return __builtin_mul_overflow(a, b, &r) ? INT64_MAX : r;
 }
 
-struct Batch {
-  const int32_t *q_start, *kv_len, *block_table;
-  const float *k_scale, *v_scale;
-  void *k, *v;
-};
-
-bool arity(Py_ssize_t n, Py_ssize_t want) {
-  if (n == want) return true;
-  PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
-  return false;
-}
-
 // qkv T Hq Hkv qw kw cos_sin max_pos rope eps | q_start kv_len B table max_pages page n_pages dtype ks vs | q_out k v
 // status head_dim stream
-PyObject* paged_kv(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  if (!arity(n, 26)) return nullptr;
+PyObject* paged_kv_call(PyObject* const* v) {
   Args a{v, device_now()};
   const int32_t T = a.i32(1), hq = a.i32(2), hkv = a.i32(3), max_pos = a.i32(7), rope = a.truth(8), B = a.i32(12),
                 mp = a.i32(14), ps = a.i32(15), dt = a.i32(17), dh = a.i32(24);
@@ -186,8 +191,7 @@ PyObject* paged_kv(PyObject*, PyObject* const* v, Py_ssize_t n) {
 
 // q T | q_start kv_len B table max_pages page n_pages | k v dtype ks vs | Hq Hkv max_q window scale out ws status
 // head_dim stream
-PyObject* paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  if (!arity(n, 24)) return nullptr;
+PyObject* paged_attention_call(PyObject* const* v) {
   Args a{v, device_now()};
   const int32_t T = a.i32(1), B = a.i32(4), mp = a.i32(6), ps = a.i32(7), dt = a.i32(11), hq = a.i32(14),
                 hkv = a.i32(15), max_q = a.i32(16), window = a.i32(17), dh = a.i32(22);
@@ -215,8 +219,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
 }
 
 // logits rows vocab row_stride dtype temperature top_k top_p min_p u tokens logprobs status stream
-PyObject* sample(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  if (!arity(n, 14)) return nullptr;
+PyObject* sample_call(PyObject* const* v) {
   Args a{v, device_now()};
   const int32_t rows = a.i32(1), vocab = a.i32(2), dt = a.i32(4);
   const int64_t stride = a.i(3), per_row = rows > 0 ? 4 * static_cast<int64_t>(rows) : 0;
@@ -234,6 +237,12 @@ PyObject* sample(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (a.bad) return nullptr;
   return finish(flint_sample(x, rows, vocab, stride, dt, t, k, p, m, u, tok, lp, st, stream));
 }
+
+PyObject* paged_kv(PyObject* m, PyObject* const* v, Py_ssize_t n) { return guarded<paged_kv_call>(m, v, n, 26); }
+PyObject* paged_attention(PyObject* m, PyObject* const* v, Py_ssize_t n) {
+  return guarded<paged_attention_call>(m, v, n, 24);
+}
+PyObject* sample(PyObject* m, PyObject* const* v, Py_ssize_t n) { return guarded<sample_call>(m, v, n, 14); }
 
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_XDECREF(g_error);

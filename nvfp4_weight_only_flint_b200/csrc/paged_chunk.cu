@@ -718,10 +718,13 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
       }
       if (!ok) break;
       const int32_t* table = p.b.block_table + static_cast<size_t>(im.s) * p.b.max_pages;
-      // pool row of this lane's box of key tile kt, -1 past the sequence
+      // pool row of this lane's box of key tile kt, -1 past the sequence; a box
+      // wholly in front of the pair's window is zeros (its page may be gone)
+      const int reach = p.window > 0 ? im.kv - im.n + im.tok0 - p.window + 1 : 0;
       auto box_row = [&](int kt) {
         const int key = kt * kTile + my_box * box;
         if (!mine || kt >= im.kt1 || key >= im.kv) return -1;
+        if (key + box <= reach) return bad_row;
         const int page = __ldg(table + (key >> p.b.page_shift));
         if (page < 0 || page >= p.b.n_pages) {
           if (half == 0) atomicOr(status, FLINT_DEVCHECK_INDEX);

@@ -37,6 +37,22 @@ def test_decode_window(window, e4m3):
     R.check_attention(R.run_attention(b, window), b, window, what=f"window {window}")
 
 
+@pytest.mark.parametrize("new", [[2, 1], [60, 40]])
+def test_window_does_not_need_pages_in_front_of_it(new):
+    # a sliding-window layer gives pages back: their table entries are no pages
+    for e4m3 in (False, True):
+        b = R.Paged(55, new, [700, 333], 8, 2, 16, e4m3)
+        whole = R.attention(b, 100)
+        for s in range(2):
+            first = b.kv[s] - b.new[s] - 100 + 1  # first key any new token sees
+            b.table[s, :first // 16] = -1
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = R.run_attention(b, 100, status=st)
+        assert int(st.item()) == 0
+        assert torch.equal(R.attention(b, 100), whole)
+        R.check_attention(got, b, 100, what="freed pages")
+
+
 def test_decode_peaked_scores():
     b = R.Paged(50, [1, 1], [3000, 200], q_gain=5.0)
     R.check_attention(R.run_attention(b), b, what="peaked")

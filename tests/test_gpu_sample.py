@@ -228,3 +228,17 @@ def test_sample_repeats_and_replays():
         fm.flint_sample(x, 16, 150144, 150144, fm.FLINT_LOGITS_F32, t, k, p, m, u, tok2, None)
     torch.cuda.synchronize()
     assert torch.equal(tok, first[0]) and torch.equal(tok2, first[0])
+
+
+def test_sample_refuses_tensors_it_would_read_wrongly():
+    x = torch.zeros((4, 200), device="cuda")
+    u, tok = torch.zeros(4, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    call = lambda **k: fm.flint_sample(**{**dict(logits=x, rows=4, vocab=200, row_stride=200,  # noqa: E731
+                                                 logits_dtype=fm.FLINT_LOGITS_F32, temperature=None, top_k=None,
+                                                 top_p=None, min_p=None, u=u, tokens=tok), **k})
+    call()
+    for bad in (dict(logits=x[:, ::2]), dict(logits=x[:2]), dict(u=u[:3]), dict(tokens=tok.cpu()), dict(row_stride=300),
+                dict(logits=x.to_sparse()), dict(top_k=torch.zeros(3, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(fm.FlintError) as e:
+            call(**bad)
+        assert e.value.code == -1

@@ -104,5 +104,17 @@ def test_sample_arguments(L):
 def test_python_wrappers_refuse_cpu_tensors():
     import torch
     x = torch.zeros(1000)
-    with pytest.raises(fm.FlintError):
+    with pytest.raises(fm.FlintError) as e:
         fm.flint_sample(x, 1, 100, 100, fm.FLINT_LOGITS_F32, None, None, None, None, x, x)
+    assert e.value.code == -1 and "logits" in str(e.value)
+    with pytest.raises(fm.FlintError):  # torch's own exceptions do not leave the marshalling
+        fm.flint_sample(x.to_sparse(), 1, 100, 100, fm.FLINT_LOGITS_F32, None, None, None, None, x, x)
+    with pytest.raises(fm.FlintError):
+        fm.flint_sample(A, 1 << 40, 100, 100, fm.FLINT_LOGITS_F32, None, None, None, None, A, A, stream=0)
+    with pytest.raises(fm.FlintError):
+        fm.flint_qk_norm_rope_paged_kv(x, 1, 1, 1, None, None, None, 0, False, 0.0, x, x, 1, x, 1, 16, 4,
+                                       fm.FLINT_KV_BF16, None, None, x, x, x)
+    with pytest.raises(fm.FlintError):
+        fm.flint_paged_attention(x, 1, x, x, 1, x, 1, 16, 4, x, x, fm.FLINT_KV_BF16, None, None, 1, 1, 1, 0, 0.1, x, x)
+    with pytest.raises(TypeError):
+        fm.flint_sample("logits", 1, "many", 100, 0, None, None, None, None, x, x)
