@@ -275,6 +275,11 @@ struct Share {
   }
 };
 
+__device__ __forceinline__ bool any_in(const float (&x)[4], float lo, float hi) {
+  return (x[0] >= lo && x[0] <= hi) || (x[1] >= lo && x[1] <= hi) || (x[2] >= lo && x[2] <= hi) ||
+         (x[3] >= lo && x[3] <= hi);
+}
+
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -296,6 +301,7 @@ __device__ __forceinline__ void hist_pass(Shared& sh, const S s, uint32_t klo, u
   for (int i = 4 * threadIdx.x; i < n; i += 4 * kThreads) {
     float x[4];
     s.get4(i, n, x);
+    if (b1 >= 0 && !any_in(x, xlo, xhi)) continue;  // most of a later level's tokens
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (!(x[q] >= xlo && x[q] <= xhi)) continue;
@@ -433,7 +439,7 @@ __device__ __forceinline__ void gather(Shared& sh, const S s, float from, float 
   for (int i = 4 * threadIdx.x; i < n; i += 4 * kThreads) {
     float x[4];
     s.get4(i, n, x);
-    if (!(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)) continue;
+    if (!any_in(x, from, to)) continue;
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       const float y = q == 0 ? x[0] : q == 1 ? x[1] : q == 2 ? x[2] : x[3];
