@@ -534,8 +534,8 @@ int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t* q_start, 
  * with w_i >= min_p (the largest always). The token is the first index, in
  * vocabulary order, whose running sum of kept w exceeds u times the kept total;
  * its log-probability is ln(w / kept total). Masses are summed as integers of
- * 2^-44 of the largest (coarser above 2^18 tokens): the result is the same in
- * every run, and a token below half of that is never drawn.
+ * 2^-45 of the largest (at 2^18 tokens; finer below, coarser above): the result
+ * is the same in every run, and a token below half of that is never drawn.
  *   status      nullable device int32. A row without any logit above -inf sets
  *               FLINT_DEVCHECK_NONFINITE, one with a negative or NaN temperature
  *               or u outside [0, 1) FLINT_DEVCHECK_INDEX; both give token -1,

@@ -32,7 +32,7 @@
 //
 // Masses are sums of integers w 2^s (s = 44 for 150,144 tokens), 64 bits wide:
 // the same in any order, so a run's result does not depend on the order of the
-// shared-memory atomics; a token below 2^-45 of the largest is never drawn, far
+// shared-memory atomics; a token below 2^-46 of the largest is never drawn, far
 // below what a 24-bit u can reach. Each w is right to 2^-27 of itself: a flat
 // row of 150,144 tokens has its running sums within 1e-6 of one token's width
 // (plain fp32 weights: 3e-5, a wrong token in one row of 15,000). Whole rows are
@@ -85,6 +85,7 @@ struct SampleParams {
   int32_t* status;
   long long stride;
   int V, slice, up;
+  double far;  // s + 2
 };
 
 // Order-preserving integer of a clean float (no NaN, no -0) and back.
@@ -136,7 +137,7 @@ __device__ __forceinline__ uint32_t shift_right(uint32_t x, int n) {
 // than 32 drops is half a unit of 2^-s on average, which the last bit stands for
 // (units of 2^-(s + 1)); equal large weights stay multiples of 2^17, so their
 // sums and shares of them are exact.
-// Tokens below `far` (2^-60 of the largest; masked ones) have no mass.
+// Tokens below `far` (2^-(s + 2) of the largest; masked ones) have no mass.
 struct Scale {
   double c, k;  // 2^26 log2(e) / T;  1.5 2^52 + 63 2^26 - c x_max
   float far;
@@ -152,7 +153,7 @@ struct Scale {
     // adding 2^23 rounds 2^28 2^(j/64) (2^f - 1) < 2^23 to an integer in the low bits
     const uint32_t w =
         static_cast<uint32_t>(t.i + static_cast<int>(__float_as_uint(fmaf(q, t.f, 8388608.f)) - 0x4B000000u));
-    const int sh = up - static_cast<int>(z >> 26);  // 15 or more
+    const int sh = up - static_cast<int>(z >> 26);  // 3 or more
     const uint32_t lo = shift_right(__funnelshift_rc(0u, w, sh), max(sh - 32, 0)), hi = shift_right(w, sh);
     const u64 m = (static_cast<u64>(hi) << 32) | lo | (sh > 32 ? 1u : 0u);
     return x >= far ? m : 0;
@@ -973,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     const double c = fmin(0x1p26 / ln_unit, 1e38);
     r.sc.c = c;
     r.sc.k = 6755399441055744.0 + 63.0 * 0x1p26 - c * static_cast<double>(x_max);
-    r.sc.far = fminf(x_max, __double2float_ru(static_cast<double>(x_max) - 60.0 * ln_unit));
+    r.sc.far = fminf(x_max, __double2float_ru(static_cast<double>(x_max) - p.far * ln_unit));
     if (!(r.sc.far > -INFINITY)) r.sc.far = -FLT_MAX;  // an infinite T: every token that is not masked
     r.sc.up = p.up;
     r.x_max = x_max;
@@ -1094,10 +1095,11 @@ extern "C" int flint_sample(const void* logits, int32_t rows, int32_t vocab, int
   p.V = vocab;
   int lg = 0;
   while ((1 << lg) < vocab) ++lg;
-  const int mass_bits = 62 - lg < 44 ? 62 - lg : 44;  // the row's mass stays below 2^63
+  const int mass_bits = 62 - lg < 56 ? 62 - lg : 56;  // the row's mass, in units of 2^-(s + 1), stays below 2^63
   static const ExpTable table;
   for (int j = 0; j < 64; ++j) p.exp2_tab[j] = table.v[j];
   p.up = 63 + 32 - (mass_bits + 1 - 28);
+  p.far = mass_bits + 2;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       logits_dtype == FLINT_LOGITS_F32 ? launch<float>(p, rows, st) : launch<uint16_t>(p, rows, st);
