@@ -986,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     r.cut_ties = r.cut_count = 0;
     // min-p: w >= min_p is x >= x_max + T ln(min_p), up to the next float
     r.least = -INFINITY;
-    if (min_p > 0.f)
+    if (min_p > 0.f && T < INFINITY)
       r.least = fminf(x_max, __double2float_ru(static_cast<double>(x_max) +
                                                static_cast<double>(T) * log(fmin(static_cast<double>(min_p), 1.0))));
     r.n = n;

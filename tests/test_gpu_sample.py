@@ -1,9 +1,9 @@
 """Sampling against its 64-bit form, row by row: every filter alone and together, vocabularies from one token to more
 than shared memory holds, ties, masked rows, infinities, NaN, extreme temperatures, strides, both logit types.
 
-Tokens have to be equal: each weight is right to 2^-28 of itself and the sums are exact, so a token could differ only
-where u, top_p or min_p falls within 2^-28 of a border (less than 1e-6 a row), which these seeds do not meet.
-Log-probabilities: the ratio of a weight and a sum, each right to 2^-28 (2^-27 absolute in the logarithm), and the fp32
+Tokens have to be equal: each weight is right to 2^-27 of itself and the sums are exact, so a token could differ only
+where u, top_p or min_p falls within 2^-27 of a border (less than 1e-6 a row), which these seeds do not meet.
+Log-probabilities: the ratio of a weight and a sum, each right to 2^-27 (2^-26 absolute in the logarithm), and the fp32
 rounding of the result (2^-24 relative)."""
 import math
 
@@ -148,10 +148,16 @@ def test_sample_masked_rows_and_infinities():
     assert set(tok.tolist()) <= want and abs(float(lp[0]) + math.log(160)) < 1e-6
 
 
-@pytest.mark.parametrize("t", [1e-44, 1e-30, 1e-3, 0.05, 20.0, 1e6])
+@pytest.mark.parametrize("t", [1e-44, 1e-30, 1e-3, 0.05, 20.0, 1e6, math.inf])
 def test_sample_extreme_temperatures(t):
     x = _logits(21, 4, 20_000)
     _check(x, [t] * 4, [0, 500, 0, 0], [1.0, 0.9, 0.9, 1.0], [0.0, 0.0, 0.0, 0.3], _u(22, 4))
+
+
+def test_sample_infinite_temperature_with_min_p():
+    # every weight is 1: min-p of 1 keeps them all
+    x = _logits(23, 4, 5000)
+    _check(x, [math.inf] * 4, [0, 0, 700, 20], [1.0, 0.9, 1.0, 1.0], [1.0, 1.0, 2.0, 0.5], _u(24, 4))
 
 
 @pytest.mark.parametrize("k", [255, 256, 257, 511, 512, 513, 1024, 1025, 3000])
