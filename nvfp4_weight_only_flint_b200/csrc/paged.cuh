@@ -64,11 +64,10 @@ inline bool paged_aligned16(const void* q) { return (reinterpret_cast<uintptr_t>
 
 // Host side: checks the batch's arguments and fills `b`; FLINT_OK, or the
 // recorded error.
-inline int paged_batch(PagedBatch* b, const char* who, int32_t T, const int32_t* q_start, const int32_t* kv_len,
-                       int32_t B, const int32_t* block_table, int32_t max_pages, int32_t page_size, int64_t n_pages,
+inline int paged_batch(PagedBatch* b, int32_t T, const int32_t* q_start, const int32_t* kv_len, int32_t B,
+                       const int32_t* block_table, int32_t max_pages, int32_t page_size, int64_t n_pages,
                        int32_t cache_dtype, const void* k_cache, const void* v_cache, const float* k_scale,
                        const float* v_scale) {
-  (void)who;
   if (page_size < kPagedMinPage || page_size > kPagedMaxPage || (page_size & (page_size - 1)) != 0)
     return flint_fail_external(FLINT_ERR_UNSUPPORTED_SHAPE, "page_size must be a power of two in 16..1024");
   if (cache_dtype != FLINT_KV_BF16 && cache_dtype != FLINT_KV_E4M3)

@@ -189,7 +189,7 @@ extern "C" int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32
   if (n_q_heads > 65535 || n_kv_heads > 65535)
     return flint_fail_external(FLINT_ERR_UNSUPPORTED_SHAPE, "at most 65535 heads");
   AppendParams p{};
-  const int rc = paged_batch(&p.b, "flint_qk_norm_rope_paged_kv", T, q_start, kv_len, B, block_table, max_pages,
+  const int rc = paged_batch(&p.b, T, q_start, kv_len, B, block_table, max_pages,
                              page_size, n_pages, cache_dtype, k_cache, v_cache, k_scale, v_scale);
   if (rc != FLINT_OK) return rc;
   if (T == 0 || B == 0) return FLINT_OK;
