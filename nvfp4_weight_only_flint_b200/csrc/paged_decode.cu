@@ -20,15 +20,25 @@
 // blocks of 16 keys through a cp.async ring; page ids are read 32 at a time,
 // one batch ahead. Rows of a block past the end are filled with zeros, so
 // whatever an unused cache row holds never reaches the sums.
-//   bf16 cache: S = Q K^T by ldmatrix on key rows, P rounded to bf16, V by
-//     ldmatrix.trans (rows padded to 272 bytes: conflict-free).
+// The products are taken transposed, keys and dimensions as the 16 rows of an
+// MMA and the query rows as its 8 columns (two column tiles above 8 rows), so
+// that no half of a tile is empty for a group of 8:
+//   S^T [16 keys][8] = K Q^T      8 MMAs per 16 keys
+//   O^T [16 dims][8] += V^T P^T   8 MMAs, P^T by movmatrix from S^T's layout
+//   bf16 cache: K by ldmatrix on key rows, V by ldmatrix.trans (rows padded to
+//     272 bytes: conflict-free), P rounded to bf16.
 //   E4M3 cache: codes become f16 (exact) on the way into the fragments. The
-//     order of the 128 terms of q . k and of the output columns is free, so a
-//     thread reads 16-byte runs of a key row (K) and 16-byte runs of the four
+//     order of the 128 terms of q . k and of the output's dimensions is free, so
+//     a thread reads 16-byte runs of a key row (K) and 16-byte runs of the four
 //     keys it holds weights for (V) and needs no transpose; Q is f16 after an
 //     exact power-of-two scale per row, P is f16. 128-byte rows whose 16-byte
 //     pieces are permuted by the row number (piece_of): conflict-free for
 //     both reads without padding.
+// (Query rows as the 16 rows of a tile: twice the MMAs and accumulators; 8 x
+// 32K of E4M3 58.9 us against 53.5, 64 ragged bf16 sequences 98.8 with both.)
+// 8 x 32K of E4M3: 4.8 TB/s. Two blocks a step 53.9 us, three CTAs an SM 53.8
+// (both 52.9): the warps then wait for memory, and the SMs are active for 80
+// to 88 % of the kernel's time.
 // The running sum adds the rounded weights, so the output stays a convex
 // combination of the values.
 #include "paged_attn.cuh"
@@ -40,7 +50,7 @@ constexpr int kDh = kPagedHeadDim;
 constexpr int kWarps = 4;
 constexpr int kBlock = 16;
 constexpr int kQuantum = kWarps * kBlock;
-constexpr int kCtaSlots = 2 * 148;  // two CTAs per SM (three of an E4M3 cache, 168 registers and four stages: 61 us against 58)
+constexpr int kCtaSlots = 2 * 148;  // two CTAs per SM
 constexpr int kRowsMax = kDecodeRows;
 
 template <bool kE4M3>
@@ -74,6 +84,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t& r0, uint32_t& r1
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
                : "r"(addr));
 }
+// 8 x 8 transpose of 16-bit values across the warp (a thread's register: row lane / 4, columns 2 (lane % 4) ..)
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 template <bool kF16>
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (kF16)
@@ -104,6 +120,11 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ uint32_t piece_of(int r, int c) {
   return static_cast<uint32_t>(c ^ ((((r >> 1) & 3) << 1) ^ ((r & 1) << 2))) << 4;
 }
+
+// Place of dimension d of row r where the warps meet: the four row pairs that a
+// warp stores at once take different banks.
+template <bool kE4M3>
+__device__ __forceinline__ int met_at(int r, int d) { return d ^ (((r >> 1) & 3) * (kE4M3 ? 4 : 8)); }
 
 // A sequence on the line: its keys [first, kv) in quanta of 64.
 struct Line {
@@ -287,18 +308,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
       cp_commit();
     }
 
-    // ---- Q fragments; row r of the tile is token r / group, head r % group
-    uint32_t qa[8][4];
-    float sc[2] = {p.scale * kLog2e, p.scale * kLog2e};
-    int lim[2];  // keys below lim[x] and from lim[x] - window on are attended
+    // ---- Q^T fragments: this lane's column gq of column tile x is row 8 x + gq; row r is token r / group, head r %
+    // group. Softmax state: rows 8 x + 2 t4 + {0, 1}, as in the accumulators.
+    constexpr int kNt = kTall ? 2 : 1;
+    uint32_t qb[8][kNt][2];
+    float sc[kNt][2];
+    int lim[kNt][2];  // keys below lim and from lim - window on are attended
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < kNt; ++x) {
       const int r = gq + 8 * x;
       const int tok = r / p.group, h = r - tok * p.group;
-      const bool live = (x == 0 || kTall) && tok < n;
-      lim[x] = live ? kv - n + tok + 1 : 0;
+      const bool live = tok < n;
       const uint16_t* qh =
           p.q + (static_cast<size_t>(ln.sq.row0 + (live ? tok : 0)) * p.Hq + g * p.group + (live ? h : 0)) * kDh;
+      float scale = p.scale * kLog2e;
       if constexpr (kE4M3) {
         uint4 w[4];  // 64h + 16 t4 + 0..7 and 8..15 of both halves
 #pragma unroll
@@ -316,7 +339,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const float sig = pow2_scale_for(amax);
-        sc[x] = sc[x] * __ldg(p.k_scale + g) / sig;
+        scale = scale * __ldg(p.k_scale + g) / sig;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -326,27 +349,39 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
             f[j] = pack_f16x2(__uint_as_float(u[j] << 16) * sig, __uint_as_float(u[j] & 0xFFFF0000u) * sig);
           // k-step 4 (i / 2) + 2 (i % 2) + {0, 1}: elements 4w .. 4w + 3 of the run
           const int ks = 4 * (i >> 1) + 2 * (i & 1);
-          qa[ks][x] = f[0];
-          qa[ks][2 + x] = f[1];
-          qa[ks + 1][x] = f[2];
-          qa[ks + 1][2 + x] = f[3];
+          qb[ks][x][0] = f[0];
+          qb[ks][x][1] = f[1];
+          qb[ks + 1][x][0] = f[2];
+          qb[ks + 1][x][1] = f[3];
         }
       } else {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          qa[ks][x] = live ? __ldg(reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * t4)) : 0u;
-          qa[ks][2 + x] = live ? __ldg(reinterpret_cast<const uint32_t*>(qh + 16 * ks + 8 + 2 * t4)) : 0u;
+          qb[ks][x][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * t4)) : 0u;
+          qb[ks][x][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(qh + 16 * ks + 8 + 2 * t4)) : 0u;
         }
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ri = 8 * x + 2 * t4 + i, ti = ri / p.group;
+        sc[x][i] = __shfl_sync(0xffffffffu, scale, (2 * t4 + i) * 4);
+        lim[x][i] = ti < n ? kv - n + ti + 1 : 0;
+      }
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    // rows 8 .. 15 of a low tile stay zero (their weights are): the accumulators
-    // of both halves are kept all the same, so that none has to be cleared
-    float o[16][4];
+    float m[kNt][2], l[kNt][2];  // l: this lane's keys only, until the end
+    float o[8][kNt][4];
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int x = 0; x < kNt; ++x) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[j][c] = 0.f;
+      for (int i = 0; i < 2; ++i) {
+        m[x][i] = -INFINITY;
+        l[x][i] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[j][x][c] = 0.f;
+    }
 
     for (int b = 0; b < n_blocks; ++b) {
       if (b + R::kStages - 1 < n_blocks) load_block(b + R::kStages - 1);
@@ -356,8 +391,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
       const uint32_t kr = ring + (b % R::kStages) * stage_bytes<kE4M3>();
       const uint32_t vr = kr + kBlock * R::kRowBytes;
       // two accumulators a column tile: shorter chains
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-      float u0[4] = {0.f, 0.f, 0.f, 0.f}, u1[4] = {0.f, 0.f, 0.f, 0.f};
+      float st[kNt][2][4];
+#pragma unroll
+      for (int x = 0; x < kNt; ++x)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) st[x][0][c] = st[x][1][c] = 0.f;
       if constexpr (kE4M3) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -367,106 +405,112 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            mma16<true>(w & 1 ? u0 : s0, qa[4 * half + w], e4m3x2_to_f16x2(wa[w]), e4m3x2_to_f16x2(wa[w] >> 16));
-            mma16<true>(w & 1 ? u1 : s1, qa[4 * half + w], e4m3x2_to_f16x2(wc[w]), e4m3x2_to_f16x2(wc[w] >> 16));
+            const uint32_t a[4] = {e4m3x2_to_f16x2(wa[w]), e4m3x2_to_f16x2(wc[w]), e4m3x2_to_f16x2(wa[w] >> 16),
+                                   e4m3x2_to_f16x2(wc[w] >> 16)};
+#pragma unroll
+            for (int x = 0; x < kNt; ++x)
+              mma16<true>(st[x][w & 1], a, qb[4 * half + w][x][0], qb[4 * half + w][x][1]);
           }
         }
       } else {
-        const int mr = (lane & 7) + ((lane >> 4) << 3), mc = ((lane >> 3) & 1) * 16;
+        // matrices: (keys 0-7, dims 0-7), (keys 8-15, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, dims 8-15)
+        const int mr = (lane & 7) + ((lane >> 3) & 1) * 8, mc = (lane >> 4) * 16;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          uint32_t b00, b01, b10, b11;
-          ldsm4(kr + mr * R::kRowBytes + 32 * ks + mc, b00, b01, b10, b11);
-          mma16<false>(ks & 1 ? u0 : s0, qa[ks], b00, b01);
-          mma16<false>(ks & 1 ? u1 : s1, qa[ks], b10, b11);
+          uint32_t a[4];
+          ldsm4(kr + mr * R::kRowBytes + 32 * ks + mc, a[0], a[1], a[2], a[3]);
+#pragma unroll
+          for (int x = 0; x < kNt; ++x) mma16<false>(st[x][ks & 1], a, qb[ks][x][0], qb[ks][x][1]);
         }
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        s0[c] += u0[c];
-        s1[c] += u1[c];
-      }
-      // this lane: keys 2 t4, 2 t4 + 1 (s0) and 8 + 2 t4, 9 + 2 t4 (s1) of rows gq (c 0, 1), gq + 8 (c 2, 3)
+      // this lane: keys gq (c 0, 1) and gq + 8 (c 2, 3) of rows 8 x + 2 t4 + {0, 1}
       const int kb = w0 + b * kBlock;
       const bool edge = kb + kBlock > min(w1, kv - n + 1) || (p.window > 0 && kb < kv - p.window);
-      uint32_t pa[4] = {0u, 0u, 0u, 0u};
-      float alpha[2] = {1.f, 1.f};
+      uint32_t pb[kNt][2];
+      float alpha[kNt][2];
+      bool moved = false;
 #pragma unroll
-      for (int x = 0; x < (kTall ? 2 : 1); ++x) {
-        float v[4] = {s0[2 * x] * sc[x], s0[2 * x + 1] * sc[x], s1[2 * x] * sc[x], s1[2 * x + 1] * sc[x]};
+      for (int x = 0; x < kNt; ++x) {
+        float v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = (st[x][0][c] + st[x][1][c]) * sc[x][c & 1];
         if (edge) {
-          const int hi = min(lim[x], w1), lo = p.window > 0 ? lim[x] - p.window : 0;
-          const int ki[4] = {kb + 2 * t4, kb + 2 * t4 + 1, kb + 8 + 2 * t4, kb + 9 + 2 * t4};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (ki[j] >= hi || ki[j] < lo) v[j] = -INFINITY;
-        }
-        float bm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-        const float mn = fmaxf(m[x], bm);
-        const float ms = mn == -INFINITY ? 0.f : mn;  // a row that has seen no key yet
-        alpha[x] = exp2_ftz(m[x] - ms);
-        m[x] = mn;
-        const float e0 = exp2_ftz(v[0] - ms), e1 = exp2_ftz(v[1] - ms), e2 = exp2_ftz(v[2] - ms),
-                    e3 = exp2_ftz(v[3] - ms);
-        float ps;
-        if constexpr (kE4M3) {
-          // 11 significant bits; weights below 2^-25 of the largest vanish
-          pa[x] = pack_f16x2(e0, e1);
-          pa[2 + x] = pack_f16x2(e2, e3);
-          const float2 u0 = __half22float2(*reinterpret_cast<const __half2*>(&pa[x]));
-          const float2 u1 = __half22float2(*reinterpret_cast<const __half2*>(&pa[2 + x]));
-          ps = (u0.x + u0.y) + (u1.x + u1.y);
-        } else {
-          pa[x] = bf2(e0, e1);
-          pa[2 + x] = bf2(e2, e3);
-          ps = (__uint_as_float(pa[x] << 16) + __uint_as_float(pa[x] & 0xFFFF0000u)) +
-               (__uint_as_float(pa[2 + x] << 16) + __uint_as_float(pa[2 + x] & 0xFFFF0000u));
-        }
-        ps += __shfl_xor_sync(0xffffffffu, ps, 1);
-        ps += __shfl_xor_sync(0xffffffffu, ps, 2);
-        l[x] = fmaf(l[x], alpha[x], ps);
-      }
-      // the maxima rarely move after the first blocks
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          o[j][0] *= alpha[0];
-          o[j][1] *= alpha[0];
-          if constexpr (kTall) {
-            o[j][2] *= alpha[1];
-            o[j][3] *= alpha[1];
+          for (int c = 0; c < 4; ++c) {
+            const int key = kb + gq + 8 * (c >> 1), hi = min(lim[x][c & 1], w1);
+            if (key >= hi || (p.window > 0 && key < lim[x][c & 1] - p.window)) v[c] = -INFINITY;
           }
         }
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float bm = fmaxf(v[i], v[2 + i]);
+          bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
+          bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
+          bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
+          const float mn = fmaxf(m[x][i], bm);
+          const float ms = mn == -INFINITY ? 0.f : mn;  // a row that has seen no key yet
+          alpha[x][i] = exp2_ftz(m[x][i] - ms);
+          moved = moved || mn != m[x][i];
+          m[x][i] = mn;
+          e[i] = exp2_ftz(v[i] - ms);
+          e[2 + i] = exp2_ftz(v[2 + i] - ms);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // keys gq + 8 k
+          uint32_t pk;
+          float p0, p1;
+          if constexpr (kE4M3) {
+            // 11 significant bits; weights below 2^-25 of the largest vanish
+            pk = pack_f16x2(e[2 * k], e[2 * k + 1]);
+            const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&pk));
+            p0 = u.x;
+            p1 = u.y;
+          } else {
+            pk = bf2(e[2 * k], e[2 * k + 1]);
+            p0 = __uint_as_float(pk << 16);
+            p1 = __uint_as_float(pk & 0xFFFF0000u);
+          }
+          l[x][0] = k == 0 ? fmaf(l[x][0], alpha[x][0], p0) : l[x][0] + p0;
+          l[x][1] = k == 0 ? fmaf(l[x][1], alpha[x][1], p1) : l[x][1] + p1;
+          pb[x][k] = transpose8(pk);
+        }
       }
-      auto pv = [&](int j, uint32_t b0, uint32_t b1) { mma16<kE4M3>(o[j], pa, b0, b1); };
+      // the maxima rarely move after the first blocks
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int x = 0; x < kNt; ++x)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[j][x][c] *= alpha[x][c & 1];
+      }
       if constexpr (kE4M3) {
-        // codes 16 gq .. 16 gq + 15 of keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4:
-        // MMA column gq of tile j is dimension 16 gq + j
+        // codes 16 gq .. 16 gq + 15 of keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4: rows gq and gq + 8 of MMA tile j are
+        // dimensions 16 gq + 2 j and 16 gq + 2 j + 1
         const uint32_t pe = piece_of(2 * t4, gq), po = piece_of(2 * t4 + 1, gq);
         const uint4 v0 = lds16(vr + (2 * t4) * kDh + pe), v1 = lds16(vr + (2 * t4 + 1) * kDh + po);
         const uint4 v2 = lds16(vr + (8 + 2 * t4) * kDh + pe), v3 = lds16(vr + (9 + 2 * t4) * kDh + po);
         const uint32_t a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
         const uint32_t a2[4] = {v2.x, v2.y, v2.z, v2.w}, a3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int j = 0; j < 8; ++j) {  // bytes 2 (j % 2), 2 (j % 2) + 1 of both keys of a pair
+          const uint32_t x0 = __byte_perm(a0[j >> 1], a1[j >> 1], j & 1 ? 0x7362 : 0x5140);
+          const uint32_t x1 = __byte_perm(a2[j >> 1], a3[j >> 1], j & 1 ? 0x7362 : 0x5140);
+          const uint32_t a[4] = {e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(x1),
+                                 e4m3x2_to_f16x2(x1 >> 16)};
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {  // bytes 2 half, 2 half + 1 of both keys of a pair
-            const uint32_t x0 = __byte_perm(a0[w], a1[w], half ? 0x7362 : 0x5140);
-            const uint32_t x1 = __byte_perm(a2[w], a3[w], half ? 0x7362 : 0x5140);
-            pv(4 * w + 2 * half, e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(x1));
-            pv(4 * w + 2 * half + 1, e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(x1 >> 16));
-          }
+          for (int x = 0; x < kNt; ++x) mma16<true>(o[j][x], a, pb[x][0], pb[x][1]);
         }
       } else {
-        const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vcol = (lane >> 4) * 16;
+        // matrices: (keys 0-7, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, dims 0-7), (keys 8-15, dims 8-15)
+        const int vrow = (lane & 7) + (lane >> 4) * 8, vcol = ((lane >> 3) & 1) * 16;
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          uint32_t b0a, b1a, b0b, b1b;
-          ldsm4t(vr + vrow * R::kRowBytes + 16 * j + vcol, b0a, b1a, b0b, b1b);
-          pv(j, b0a, b1a);
-          pv(j + 1, b0b, b1b);
+        for (int j = 0; j < 8; ++j) {
+          uint32_t a[4];
+          ldsm4t(vr + vrow * R::kRowBytes + 32 * j + vcol, a[0], a[1], a[2], a[3]);
+#pragma unroll
+          for (int x = 0; x < kNt; ++x) mma16<false>(o[j][x], a, pb[x][0], pb[x][1]);
         }
       }
       __syncwarp();
@@ -477,19 +521,29 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
     // ---- the warps meet: (max, sum, O) of each through its own ring
     float* s_o = reinterpret_cast<float*>(smem + warp * ring_bytes<kE4M3>());
 #pragma unroll
-    for (int x = 0; x < (kTall ? 2 : 1); ++x) {
-      const int r = gq + 8 * x;
-      if (t4 == 0) {
-        s_m[warp][r] = m[x];
-        s_l[warp][r] = l[x];
-      }
+    for (int x = 0; x < kNt; ++x) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * x + 2 * t4 + i;
+        float sum = l[x][i];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (gq == 0) {
+          s_m[warp][r] = m[x][i];
+          s_l[warp][r] = sum;
+        }
         if constexpr (kE4M3) {
-          s_o[r * kDh + 32 * t4 + j] = o[j][2 * x];
-          s_o[r * kDh + 32 * t4 + 16 + j] = o[j][2 * x + 1];
+#pragma unroll
+          for (int j = 0; j < 8; j += 2)
+            *reinterpret_cast<float4*>(s_o + r * kDh + met_at<kE4M3>(r, 16 * gq + 2 * j)) =
+                make_float4(o[j][x][i], o[j][x][2 + i], o[j + 1][x][i], o[j + 1][x][2 + i]);
         } else {
-          *reinterpret_cast<float2*>(s_o + r * kDh + 8 * j + 2 * t4) = make_float2(o[j][2 * x], o[j][2 * x + 1]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            s_o[r * kDh + met_at<kE4M3>(r, 16 * j + gq)] = o[j][x][i];
+            s_o[r * kDh + met_at<kE4M3>(r, 16 * j + gq + 8)] = o[j][x][2 + i];
+          }
         }
       }
     }
@@ -507,7 +561,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
       for (int w = 0; w < kWarps; ++w) {
         const float f = s_m[w][r] == -INFINITY ? 0.f : exp2_ftz(s_m[w][r] - M);
         tot = fmaf(s_l[w][r], f, tot);
-        acc = fmaf(reinterpret_cast<const float*>(smem + w * ring_bytes<kE4M3>())[r * kDh + tid], f, acc);
+        const float* o_w = reinterpret_cast<const float*>(smem + w * ring_bytes<kE4M3>()) + r * kDh;
+        acc = fmaf(o_w[met_at<kE4M3>(r, tid)], f, acc);
       }
       if (whole) {
         const int tok = r / p.group, h = r - tok * p.group;
