@@ -152,6 +152,27 @@ def test_decode_split_is_the_same_in_every_run_and_graph():
     assert torch.equal(out, o2)
 
 
+# 37 kv heads leave eight parts a head: sequences cut several times, parts of several sequences
+LONG = [([1] * 5, [5000, 3333, 1, 64, 900], 0), ([8, 1, 5], [5000, 2500, 1500], 0), ([1], [8192], 0), ([1], [8128], 0),
+        ([1, 2, 1], [9000, 4500, 7000], 4000), ([1] * 40, [37 + 11 * i for i in range(40)], 0)]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_decode_few_parts(case):
+    new, kv, window = LONG[case]
+    b = R.Paged(400 + case, new, kv, 74, 37, 32)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    R.check_attention(R.run_attention(b, window, status=st), b, window, what=str((new[:4], kv[:4])))
+    assert int(st.item()) == 0
+
+
+def test_decode_other_lengths_in_the_same_tables():
+    b = R.Paged(420, [1, 1, 1], [8000, 900, 300], 74, 37, 32)
+    for kv in ([5, 70, 1], [1, 1, 1], [8000, 1, 200], [7800, 130, 300], [8000, 900, 300]):
+        b.kv, b.kv_len = kv, torch.tensor(kv, dtype=torch.int32)
+        R.check_attention(R.run_attention(b), b, what=str(kv))
+
+
 CHUNK = [([17], [17]), ([1, 3], [1, 200]), ([128], [128]), ([300], [300]), ([40], [1000]), ([33, 1, 0, 150, 1], [33, 2000, 5, 700, 64]),
          ([5], [3001]), ([513, 700], [900, 701])]
 
