@@ -87,8 +87,9 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(AppendParams p) {
   bool bad;
   const PagedSeq sq = paged_seq(p.b, lo, &bad);
   const int pos = sq.kv - sq.n + (t - sq.row0);
-  // a sequence whose length cannot hold its tokens: no position, no page
-  const bool placed = sq.kv > 0 && t - sq.row0 < sq.n;
+  // a sequence whose length cannot hold its tokens: no position, no page. In a q_start that is not sorted the search
+  // may end at a sequence that begins behind t.
+  const bool placed = sq.kv > 0 && t >= sq.row0 && t - sq.row0 < sq.n;
   long long slot = -1;
   if (placed) {
     const int page = __ldg(p.b.block_table + static_cast<size_t>(lo) * p.b.max_pages + (pos >> p.b.page_shift));

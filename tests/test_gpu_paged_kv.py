@@ -150,6 +150,28 @@ def test_append_skips_what_has_no_place():
             assert torch.equal(pool[own].view(torch.int16), was[own].view(torch.int16))
 
 
+def test_append_places_nothing_by_an_unsorted_q_start():
+    # the search for a token's sequence may end at one that begins behind the token: no position, whatever lies in front
+    # of the block table (here a page of the pool) and of the angles
+    T, n_pages, max_pages = 64, 6, 2
+    front = torch.full((64 + 2 * max_pages,), 3, dtype=torch.int32, device="cuda")
+    table = front[64:].view(2, max_pages)
+    table.copy_(torch.tensor([[0, 1], [2, 4]], dtype=torch.int32))
+    cs = torch.cat([torch.full((T, R.DH), 7.0), _angles(64)]).cuda()[T:]
+    qkv = torch.randn((T, 6, R.DH), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    for q_start, kv in (([48, 49, 0], [1, 1]), ([63, 64, 0], [20, 20]), ([30, 34, 2], [4, 32])):
+        k, v = (torch.full((n_pages, 16, 1, R.DH), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        q = torch.zeros((T, 4, R.DH), dtype=torch.bfloat16, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        fm.flint_qk_norm_rope_paged_kv(qkv, T, 4, 1, None, None, cs, 64, True, EPS, i32(q_start), i32(kv), 2, table,
+                                       max_pages, 16, n_pages, fm.FLINT_KV_BF16, None, None, q, k, v, st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == fm.FLINT_DEVCHECK_INDEX
+        assert (k == 5.0).all() and (v == 5.0).all()
+        assert (q.abs() < 7.0).all()  # no angle from in front of the table
+
+
 def test_append_position_past_the_angle_table():
     b = R.Paged(9, [3], [12], 4, 2, 16)
     cs = _angles(11)  # position 11 has no angles: appended unturned, flagged
