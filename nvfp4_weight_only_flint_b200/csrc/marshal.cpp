@@ -83,16 +83,16 @@ struct Args {
     } else {
       const at::Tensor& t = THPVariable_Unpack(v[k]);
       const int64_t have = static_cast<int64_t>(t.nbytes());
-      if (!t.is_cuda()) {
-        std::snprintf(msg, sizeof msg, "%s: expected a CUDA tensor", name);
-      } else if (t.get_device() != device) {
-        std::snprintf(msg, sizeof msg, "%s: on device %d, the current one is %d", name, static_cast<int>(t.get_device()),
-                      device);
-      } else if (!t.is_contiguous()) {
+      if (!t.is_contiguous()) {
         std::snprintf(msg, sizeof msg, "%s: not contiguous", name);
       } else if (have < need) {
         std::snprintf(msg, sizeof msg, "%s: %lld bytes, %lld needed", name, static_cast<long long>(have),
                       static_cast<long long>(need));
+      } else if (!t.is_cuda()) {
+        std::snprintf(msg, sizeof msg, "%s: expected a CUDA tensor", name);
+      } else if (t.get_device() != device) {
+        std::snprintf(msg, sizeof msg, "%s: on device %d, the current one is %d", name, static_cast<int>(t.get_device()),
+                      device);
       } else {
         if (bytes != nullptr) *bytes = have;
         return t.data_ptr();
@@ -152,11 +152,17 @@ PyObject* guarded(PyObject*, PyObject* const* v, Py_ssize_t n, Py_ssize_t want) 
   return nullptr;
 }
 
-// a * b * ..., for sizes; negative factors are left to the C call's checks
+// a * b and a + b of sizes, INT64_MAX where they do not fit (no tensor has as many bytes); factors below 1 are left to
+// the C call's checks
 int64_t mul(int64_t a, int64_t b) {
   if (a <= 0 || b <= 0) return 0;
   int64_t r;
   return __builtin_mul_overflow(a, b, &r) ? INT64_MAX : r;
+}
+
+int64_t add(int64_t a, int64_t b) {
+  int64_t r;
+  return __builtin_add_overflow(a, b, &r) ? INT64_MAX : r;
 }
 
 // qkv T Hq Hkv qw kw cos_sin max_pos rope eps | q_start kv_len B table max_pages page n_pages dtype ks vs | q_out k v
@@ -223,7 +229,7 @@ PyObject* sample_call(PyObject* const* v) {
   Args a{v, device_now()};
   const int32_t rows = a.i32(1), vocab = a.i32(2), dt = a.i32(4);
   const int64_t stride = a.i(3), per_row = rows > 0 ? 4 * static_cast<int64_t>(rows) : 0;
-  const int64_t elems = rows > 0 ? mul(rows - 1, stride) + (vocab > 0 ? vocab : 0) : 0;
+  const int64_t elems = rows > 0 ? add(mul(rows - 1, stride), vocab > 0 ? vocab : 0) : 0;
   const void* x = a.p(0, "logits", mul(elems, dt == FLINT_LOGITS_F32 ? 4 : 2));
   auto t = static_cast<const float*>(a.p(5, "temperature", per_row));
   auto k = static_cast<const int32_t*>(a.p(6, "top_k", per_row));

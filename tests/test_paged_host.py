@@ -118,3 +118,13 @@ def test_python_wrappers_refuse_cpu_tensors():
         fm.flint_paged_attention(x, 1, x, x, 1, x, 1, 16, 4, x, x, fm.FLINT_KV_BF16, None, None, 1, 1, 1, 0, 0.1, x, x)
     with pytest.raises(TypeError):
         fm.flint_sample("logits", 1, "many", 100, 0, None, None, None, None, x, x)
+
+
+@pytest.mark.parametrize("rows,stride", [(3, 1 << 62), (2, (1 << 63) - 1), ((1 << 24), 1 << 40), (2, 901)])
+def test_sample_refuses_strides_past_the_tensor(rows, stride):
+    # the bytes that rows * row_stride reach, where they do not fit 64 bits either
+    import torch
+    x, per_row = torch.zeros(1000), torch.zeros(1 << 24)
+    with pytest.raises(fm.FlintError) as e:
+        fm.flint_sample(x, rows, 100, stride, fm.FLINT_LOGITS_F32, None, None, None, None, per_row, per_row)
+    assert e.value.code == -1 and "logits" in str(e.value) and "needed" in str(e.value)
