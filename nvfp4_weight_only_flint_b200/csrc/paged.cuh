@@ -67,7 +67,7 @@ inline bool paged_aligned16(const void* q) { return (reinterpret_cast<uintptr_t>
 inline int paged_batch(PagedBatch* b, int32_t T, const int32_t* q_start, const int32_t* kv_len, int32_t B,
                        const int32_t* block_table, int32_t max_pages, int32_t page_size, int64_t n_pages,
                        int32_t cache_dtype, const void* k_cache, const void* v_cache, const float* k_scale,
-                       const float* v_scale) {
+                       const float* v_scale, const int32_t* status) {
   if (page_size < kPagedMinPage || page_size > kPagedMaxPage || (page_size & (page_size - 1)) != 0)
     return flint_fail_external(FLINT_ERR_UNSUPPORTED_SHAPE, "page_size must be a power of two in 16..1024");
   if (cache_dtype != FLINT_KV_BF16 && cache_dtype != FLINT_KV_E4M3)
@@ -84,7 +84,7 @@ inline int paged_batch(PagedBatch* b, int32_t T, const int32_t* q_start, const i
   if (!paged_aligned16(k_cache) || !paged_aligned16(v_cache) ||
       ((reinterpret_cast<uintptr_t>(q_start) | reinterpret_cast<uintptr_t>(kv_len) |
         reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(k_scale) |
-        reinterpret_cast<uintptr_t>(v_scale)) & 3u))
+        reinterpret_cast<uintptr_t>(v_scale) | reinterpret_cast<uintptr_t>(status)) & 3u))
     return flint_fail_external(FLINT_ERR_MISALIGNED, "misaligned pointer");
   b->q_start = q_start;
   b->kv_len = kv_len;

@@ -32,7 +32,7 @@ extern "C" int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t
                                "at most 32768 sequences, 1024 query heads and 2^24 new tokens");
   PagedAttnParams p{};
   const int rc = paged_batch(&p.b, T, q_start, kv_len, B, block_table, max_pages, page_size,
-                             n_pages, cache_dtype, k_cache, v_cache, k_scale, v_scale);
+                             n_pages, cache_dtype, k_cache, v_cache, k_scale, v_scale, status);
   if (rc != FLINT_OK) return rc;
   if (T == 0 || B == 0) return FLINT_OK;
   if (!q || !out) return flint_fail_external(FLINT_ERR_INVALID_ARG, "flint_paged_attention: NULL pointer");

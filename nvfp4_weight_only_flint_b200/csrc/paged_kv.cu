@@ -191,7 +191,7 @@ extern "C" int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32
     return flint_fail_external(FLINT_ERR_UNSUPPORTED_SHAPE, "at most 65535 heads");
   AppendParams p{};
   const int rc = paged_batch(&p.b, T, q_start, kv_len, B, block_table, max_pages,
-                             page_size, n_pages, cache_dtype, k_cache, v_cache, k_scale, v_scale);
+                             page_size, n_pages, cache_dtype, k_cache, v_cache, k_scale, v_scale, status);
   if (rc != FLINT_OK) return rc;
   if (T == 0 || B == 0) return FLINT_OK;
   if (!qkv || !q_out || (q_norm_w == nullptr) != (k_norm_w == nullptr) || (rope && (!cos_sin || max_pos < 1)))

@@ -1079,7 +1079,8 @@ extern "C" int flint_sample(const void* logits, int32_t rows, int32_t vocab, int
   if ((reinterpret_cast<uintptr_t>(logits) & es) ||
       ((reinterpret_cast<uintptr_t>(temperature) | reinterpret_cast<uintptr_t>(top_k) |
         reinterpret_cast<uintptr_t>(top_p) | reinterpret_cast<uintptr_t>(min_p) | reinterpret_cast<uintptr_t>(u) |
-        reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(logprobs)) & 3u))
+        reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(logprobs) |
+        reinterpret_cast<uintptr_t>(status)) & 3u))
     return flint_fail_external(FLINT_ERR_MISALIGNED, "flint_sample: misaligned pointer");
   SampleParams p{};
   p.logits = logits;

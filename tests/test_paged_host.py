@@ -128,3 +128,13 @@ def test_sample_refuses_strides_past_the_tensor(rows, stride):
     with pytest.raises(fm.FlintError) as e:
         fm.flint_sample(x, rows, 100, stride, fm.FLINT_LOGITS_F32, None, None, None, None, per_row, per_row)
     assert e.value.code == -1 and "logits" in str(e.value) and "needed" in str(e.value)
+
+
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_misaligned_status(L, by):
+    # the kernels set it with a 32-bit atomic
+    assert L.flint_qk_norm_rope_paged_kv(A, 4, 32, 4, 128, A, A, A, 16, 1, 1e-6, A, A, 2, A, 8, 16, 64, 0, None, None, A,
+                                         A, A, A + by, None) == -3
+    assert L.flint_paged_attention(A, 4, A, A, 2, A, 8, 16, 64, A, A, 0, None, None, 32, 4, 128, 1, 0, 0.088, A, A,
+                                   1 << 40, A + by, None) == -3
+    assert L.flint_sample(A, 2, 100, 100, 0, A, A, A, A, A, A, A, A + by, None) == -3
