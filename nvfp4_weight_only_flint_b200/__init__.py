@@ -344,8 +344,8 @@ def flint_ep_combine(y, pair_pos, T: int, slots: int, d: int, residual, out, str
                                   _stream(stream)))
 
 
-# The serving calls check their tensors (contiguous, on the current device, large enough) and raise FlintError
-# before anything is launched; see csrc/marshal.cpp.
+# The serving calls check their tensors (element type, contiguous, large enough, on the current device) and raise
+# FlintError before anything is launched; see csrc/marshal.cpp.
 def flint_qk_norm_rope_paged_kv(qkv, T: int, n_q_heads: int, n_kv_heads: int, q_norm_w, k_norm_w, cos_sin,
                                 max_pos: int, rope: bool, eps: float, q_start, kv_len, B: int, block_table,
                                 max_pages: int, page_size: int, n_pages: int, cache_dtype: int, k_scale, v_scale,

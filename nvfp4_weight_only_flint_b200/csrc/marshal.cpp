@@ -10,8 +10,8 @@
 //
 // Every tensor is checked for what a kernel would read wrongly: it has to be a
 // contiguous CUDA tensor on the current device (whose stream the call takes)
-// of at least the bytes the call reads or writes. A plain int passes as a
-// device address.
+// of the element type the call takes and of at least the bytes it reads or
+// writes. A plain int passes as a device address.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -35,6 +35,29 @@ void raise(int code, const char* msg) {
     PyErr_SetObject(g_error != nullptr ? g_error : PyExc_RuntimeError, a);
     Py_DECREF(a);
   }
+}
+
+// Element types. 16-bit and 8-bit integers pass as the bits of bf16 and E4M3.
+enum class Kind { kAny, kI32, kF32, kBf16, kE4M3 };
+
+bool is_kind(at::ScalarType t, Kind k) {
+  switch (k) {
+    case Kind::kAny: return true;
+    case Kind::kI32: return t == at::kInt;
+    case Kind::kF32: return t == at::kFloat;
+    case Kind::kBf16: return t == at::kBFloat16 || t == at::kShort || t == at::kUInt16;
+    case Kind::kE4M3: return t == at::kFloat8_e4m3fn || t == at::kByte || t == at::kChar;
+  }
+  return false;
+}
+const char* kind_name(Kind k) {
+  return k == Kind::kI32 ? "int32" : k == Kind::kF32 ? "float32" : k == Kind::kBf16 ? "bfloat16" : "float8_e4m3fn";
+}
+Kind cache_kind(int32_t dtype) {
+  return dtype == FLINT_KV_BF16 ? Kind::kBf16 : dtype == FLINT_KV_E4M3 ? Kind::kE4M3 : Kind::kAny;
+}
+Kind logits_kind(int32_t dtype) {
+  return dtype == FLINT_LOGITS_F32 ? Kind::kF32 : dtype == FLINT_LOGITS_BF16 ? Kind::kBf16 : Kind::kAny;
 }
 
 struct Args {
@@ -70,9 +93,9 @@ struct Args {
     return t > 0;
   }
   // device address of argument k, which the call takes `need` bytes of
-  void* p(int k, const char* name, int64_t need, int64_t* bytes = nullptr) {
+  void* p(int k, const char* name, Kind kind, int64_t need, int64_t* bytes = nullptr) {
     if (bad || v[k] == Py_None) return nullptr;
-    if (PyLong_Check(v[k])) {
+    if (PyLong_Check(v[k]) && !PyBool_Check(v[k])) {
       void* a = PyLong_AsVoidPtr(v[k]);
       if (PyErr_Occurred()) bad = true;
       return a;
@@ -83,7 +106,10 @@ struct Args {
     } else {
       const at::Tensor& t = THPVariable_Unpack(v[k]);
       const int64_t have = static_cast<int64_t>(t.nbytes());
-      if (!t.is_contiguous()) {
+      if (!is_kind(t.scalar_type(), kind)) {
+        std::snprintf(msg, sizeof msg, "%s: element type %s, %s expected", name, c10::toString(t.scalar_type()),
+                      kind_name(kind));
+      } else if (!t.is_contiguous()) {
         std::snprintf(msg, sizeof msg, "%s: not contiguous", name);
       } else if (have < need) {
         std::snprintf(msg, sizeof msg, "%s: %lld bytes, %lld needed", name, static_cast<long long>(have),
@@ -91,8 +117,8 @@ struct Args {
       } else if (!t.is_cuda()) {
         std::snprintf(msg, sizeof msg, "%s: expected a CUDA tensor", name);
       } else if (t.get_device() != device) {
-        std::snprintf(msg, sizeof msg, "%s: on device %d, the current one is %d", name, static_cast<int>(t.get_device()),
-                      device);
+        std::snprintf(msg, sizeof msg, "%s: on device %d, the current one is %d", name,
+                      static_cast<int>(t.get_device()), device);
       } else {
         if (bytes != nullptr) *bytes = have;
         return t.data_ptr();
@@ -176,19 +202,22 @@ PyObject* paged_kv_call(PyObject* const* v) {
   const bool live = T > 0 && B > 0;
   const int64_t pool = mul(mul(mul(np, ps), mul(hkv, dh)), dt == FLINT_KV_E4M3 ? 1 : 2);
   const int64_t sc = dt == FLINT_KV_E4M3 ? 4 * static_cast<int64_t>(hkv) : 0;
-  auto qkv = static_cast<const uint16_t*>(a.p(0, "qkv", mul(row, hq + 2 * static_cast<int64_t>(hkv))));
-  auto qw = static_cast<const uint16_t*>(a.p(4, "q_norm_w", 2 * static_cast<int64_t>(dh)));
-  auto kw = static_cast<const uint16_t*>(a.p(5, "k_norm_w", 2 * static_cast<int64_t>(dh)));
-  auto cs = static_cast<const float*>(a.p(6, "cos_sin", rope ? mul(4 * static_cast<int64_t>(dh), max_pos) : 0));
-  auto qs = static_cast<const int32_t*>(a.p(10, "q_start", live ? 4 * (static_cast<int64_t>(B) + 1) : 0));
-  auto kl = static_cast<const int32_t*>(a.p(11, "kv_len", live ? 4 * static_cast<int64_t>(B) : 0));
-  auto bt = static_cast<const int32_t*>(a.p(13, "block_table", live ? mul(4 * static_cast<int64_t>(B), mp) : 0));
-  auto ks = static_cast<const float*>(a.p(18, "k_scale", sc));
-  auto vs = static_cast<const float*>(a.p(19, "v_scale", sc));
-  auto q_out = static_cast<uint16_t*>(a.p(20, "q_out", mul(row, hq)));
-  void* k = a.p(21, "k_cache", pool);
-  void* vv = a.p(22, "v_cache", pool);
-  auto st = static_cast<int32_t*>(a.p(23, "status", 4));
+  const Kind sk = dt == FLINT_KV_E4M3 ? Kind::kF32 : Kind::kAny;  // ignored for a bf16 cache
+  auto qkv = static_cast<const uint16_t*>(a.p(0, "qkv", Kind::kBf16, mul(row, hq + 2 * static_cast<int64_t>(hkv))));
+  auto qw = static_cast<const uint16_t*>(a.p(4, "q_norm_w", Kind::kBf16, 2 * static_cast<int64_t>(dh)));
+  auto kw = static_cast<const uint16_t*>(a.p(5, "k_norm_w", Kind::kBf16, 2 * static_cast<int64_t>(dh)));
+  auto cs = static_cast<const float*>(
+      a.p(6, "cos_sin", Kind::kF32, rope ? mul(4 * static_cast<int64_t>(dh), max_pos) : 0));
+  auto qs = static_cast<const int32_t*>(a.p(10, "q_start", Kind::kI32, live ? 4 * (static_cast<int64_t>(B) + 1) : 0));
+  auto kl = static_cast<const int32_t*>(a.p(11, "kv_len", Kind::kI32, live ? 4 * static_cast<int64_t>(B) : 0));
+  auto bt = static_cast<const int32_t*>(
+      a.p(13, "block_table", Kind::kI32, live ? mul(4 * static_cast<int64_t>(B), mp) : 0));
+  auto ks = static_cast<const float*>(a.p(18, "k_scale", sk, sc));
+  auto vs = static_cast<const float*>(a.p(19, "v_scale", sk, sc));
+  auto q_out = static_cast<uint16_t*>(a.p(20, "q_out", Kind::kBf16, mul(row, hq)));
+  void* k = a.p(21, "k_cache", cache_kind(dt), pool);
+  void* vv = a.p(22, "v_cache", cache_kind(dt), pool);
+  auto st = static_cast<int32_t*>(a.p(23, "status", Kind::kI32, 4));
   void* stream = a.stream(25);
   if (a.bad) return nullptr;
   return finish(flint_qk_norm_rope_paged_kv(qkv, T, hq, hkv, dh, qw, kw, cs, max_pos, rope, eps, qs, kl, B, bt, mp, ps,
@@ -206,18 +235,20 @@ PyObject* paged_attention_call(PyObject* const* v) {
   const bool live = T > 0 && B > 0;
   const int64_t pool = mul(mul(mul(np, ps), mul(hkv, dh)), dt == FLINT_KV_E4M3 ? 1 : 2);
   const int64_t sc = dt == FLINT_KV_E4M3 ? 4 * static_cast<int64_t>(hkv) : 0;
+  const Kind sk = dt == FLINT_KV_E4M3 ? Kind::kF32 : Kind::kAny;  // ignored for a bf16 cache
   int64_t ws_bytes = 0;
-  auto q = static_cast<const uint16_t*>(a.p(0, "q", row));
-  auto qs = static_cast<const int32_t*>(a.p(2, "q_start", live ? 4 * (static_cast<int64_t>(B) + 1) : 0));
-  auto kl = static_cast<const int32_t*>(a.p(3, "kv_len", live ? 4 * static_cast<int64_t>(B) : 0));
-  auto bt = static_cast<const int32_t*>(a.p(5, "block_table", live ? mul(4 * static_cast<int64_t>(B), mp) : 0));
-  void* k = a.p(9, "k_cache", pool);
-  void* vv = a.p(10, "v_cache", pool);
-  auto ks = static_cast<const float*>(a.p(12, "k_scale", sc));
-  auto vs = static_cast<const float*>(a.p(13, "v_scale", sc));
-  auto out = static_cast<uint16_t*>(a.p(19, "out", row));
-  void* ws = a.p(20, "workspace", 0, &ws_bytes);
-  auto st = static_cast<int32_t*>(a.p(21, "status", 4));
+  auto q = static_cast<const uint16_t*>(a.p(0, "q", Kind::kBf16, row));
+  auto qs = static_cast<const int32_t*>(a.p(2, "q_start", Kind::kI32, live ? 4 * (static_cast<int64_t>(B) + 1) : 0));
+  auto kl = static_cast<const int32_t*>(a.p(3, "kv_len", Kind::kI32, live ? 4 * static_cast<int64_t>(B) : 0));
+  auto bt = static_cast<const int32_t*>(
+      a.p(5, "block_table", Kind::kI32, live ? mul(4 * static_cast<int64_t>(B), mp) : 0));
+  void* k = a.p(9, "k_cache", cache_kind(dt), pool);
+  void* vv = a.p(10, "v_cache", cache_kind(dt), pool);
+  auto ks = static_cast<const float*>(a.p(12, "k_scale", sk, sc));
+  auto vs = static_cast<const float*>(a.p(13, "v_scale", sk, sc));
+  auto out = static_cast<uint16_t*>(a.p(19, "out", Kind::kBf16, row));
+  void* ws = a.p(20, "workspace", Kind::kAny, 0, &ws_bytes);
+  auto st = static_cast<int32_t*>(a.p(21, "status", Kind::kI32, 4));
   void* stream = a.stream(23);
   if (a.bad) return nullptr;
   return finish(flint_paged_attention(q, T, qs, kl, B, bt, mp, ps, np, k, vv, dt, ks, vs, hq, hkv, dh, max_q, window,
@@ -230,15 +261,15 @@ PyObject* sample_call(PyObject* const* v) {
   const int32_t rows = a.i32(1), vocab = a.i32(2), dt = a.i32(4);
   const int64_t stride = a.i(3), per_row = rows > 0 ? 4 * static_cast<int64_t>(rows) : 0;
   const int64_t elems = rows > 0 ? add(mul(rows - 1, stride), vocab > 0 ? vocab : 0) : 0;
-  const void* x = a.p(0, "logits", mul(elems, dt == FLINT_LOGITS_F32 ? 4 : 2));
-  auto t = static_cast<const float*>(a.p(5, "temperature", per_row));
-  auto k = static_cast<const int32_t*>(a.p(6, "top_k", per_row));
-  auto p = static_cast<const float*>(a.p(7, "top_p", per_row));
-  auto m = static_cast<const float*>(a.p(8, "min_p", per_row));
-  auto u = static_cast<const float*>(a.p(9, "u", per_row));
-  auto tok = static_cast<int32_t*>(a.p(10, "tokens", per_row));
-  auto lp = static_cast<float*>(a.p(11, "logprobs", per_row));
-  auto st = static_cast<int32_t*>(a.p(12, "status", 4));
+  const void* x = a.p(0, "logits", logits_kind(dt), mul(elems, dt == FLINT_LOGITS_F32 ? 4 : 2));
+  auto t = static_cast<const float*>(a.p(5, "temperature", Kind::kF32, per_row));
+  auto k = static_cast<const int32_t*>(a.p(6, "top_k", Kind::kI32, per_row));
+  auto p = static_cast<const float*>(a.p(7, "top_p", Kind::kF32, per_row));
+  auto m = static_cast<const float*>(a.p(8, "min_p", Kind::kF32, per_row));
+  auto u = static_cast<const float*>(a.p(9, "u", Kind::kF32, per_row));
+  auto tok = static_cast<int32_t*>(a.p(10, "tokens", Kind::kI32, per_row));
+  auto lp = static_cast<float*>(a.p(11, "logprobs", Kind::kF32, per_row));
+  auto st = static_cast<int32_t*>(a.p(12, "status", Kind::kI32, 4));
   void* stream = a.stream(13);
   if (a.bad) return nullptr;
   return finish(flint_sample(x, rows, vocab, stride, dt, t, k, p, m, u, tok, lp, st, stream));

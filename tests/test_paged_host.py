@@ -138,3 +138,76 @@ def test_misaligned_status(L, by):
     assert L.flint_paged_attention(A, 4, A, A, 2, A, 8, 16, 64, A, A, 0, None, None, 32, 4, 128, 1, 0, 0.088, A, A,
                                    1 << 40, A + by, None) == -3
     assert L.flint_sample(A, 2, 100, 100, 0, A, A, A, A, A, A, A, A + by, None) == -3
+
+
+def _sample_tensors():
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    return dict(logits=torch.zeros((4, 200)), rows=4, vocab=200, row_stride=200, logits_dtype=fm.FLINT_LOGITS_F32,
+                temperature=torch.zeros(4, dtype=f32), top_k=torch.zeros(4, dtype=i32), top_p=torch.zeros(4, dtype=f32),
+                min_p=torch.zeros(4, dtype=f32), u=torch.zeros(4, dtype=f32), tokens=torch.zeros(4, dtype=i32),
+                logprobs=torch.zeros(4, dtype=f32), status=torch.zeros(1, dtype=i32))
+
+
+def _paged_tensors(e4m3, attention):
+    import torch
+    i32, bf16 = torch.int32, torch.bfloat16
+    pool = lambda: torch.zeros((4, 16, 2, 128), dtype=torch.float8_e4m3fn if e4m3 else bf16)  # noqa: E731
+    d = dict(T=3, q_start=torch.zeros(3, dtype=i32), kv_len=torch.zeros(2, dtype=i32), B=2,
+             block_table=torch.zeros((2, 5), dtype=i32), max_pages=5, page_size=16, n_pages=4, k_cache=pool(),
+             v_cache=pool(), cache_dtype=fm.FLINT_KV_E4M3 if e4m3 else fm.FLINT_KV_BF16,
+             k_scale=torch.ones(2) if e4m3 else None, v_scale=torch.ones(2) if e4m3 else None, n_q_heads=4,
+             n_kv_heads=2, status=torch.zeros(1, dtype=i32))
+    q = lambda h: torch.zeros((3, h, 128), dtype=bf16)  # noqa: E731
+    if attention:
+        return dict(d, q=q(4), max_q_len=1, window=0, scale=0.1, out=q(4), workspace=torch.zeros(64, dtype=torch.uint8))
+    w = lambda: torch.ones(128, dtype=bf16)  # noqa: E731
+    return dict(d, qkv=q(8), q_norm_w=w(), k_norm_w=w(), cos_sin=torch.zeros((9, 128)), max_pos=9, rope=True, eps=0.0,
+                q_out=q(4))
+
+
+def _calls():
+    return [(fm.flint_sample, _sample_tensors()),
+            *[(f, _paged_tensors(e, f is fm.flint_paged_attention))
+              for f in (fm.flint_paged_attention, fm.flint_qk_norm_rope_paged_kv) for e in (False, True)]]
+
+
+def test_element_types():
+    """Each tensor of another type than the kernel reads is refused by name, wider ones (torch's default integers) too;
+    the right type gets as far as the device check. Every other tensor is an address here, so that the one under test is
+    the first to be looked at."""
+    import torch
+    for f, args in _calls():
+        for name, x in args.items():
+            if not isinstance(x, torch.Tensor):
+                continue
+            only = {k: A if isinstance(v, torch.Tensor) else v for k, v in args.items()}
+            with pytest.raises(fm.FlintError) as e:  # the right type: refused for its device only
+                f(**{**only, name: x}, stream=0)
+            assert name in str(e.value) and "CUDA tensor" in str(e.value)
+            if name == "workspace":
+                continue
+            for dt in (torch.int64, torch.float64, torch.float32, torch.int32, torch.float16, torch.bfloat16, torch.bool,
+                       torch.float8_e5m2):
+                if dt == x.dtype:
+                    continue
+                with pytest.raises(fm.FlintError) as e:
+                    f(**{**only, name: torch.zeros((x.numel() * 2,), dtype=dt)}, stream=0)
+                assert e.value.code == -1 and name in str(e.value) and "element type" in str(e.value), (name, dt)
+            with pytest.raises(fm.FlintError) as e:
+                f(**{**only, name: True}, stream=0)
+            assert name in str(e.value)
+
+
+def test_bits_of_16_and_8_bit_types():
+    import torch
+    for f, args in _calls()[1:]:
+        for name in ("q", "qkv", "q_norm_w", "out", "q_out", "k_cache", "v_cache"):
+            if name not in args:
+                continue
+            only = {k: A if isinstance(v, torch.Tensor) else v for k, v in args.items()}
+            one = args[name].element_size() == 1
+            for dt in (torch.uint8, torch.int8) if one else (torch.int16, torch.uint16):
+                with pytest.raises(fm.FlintError) as e:
+                    f(**{**only, name: args[name].view(dt)}, stream=0)
+                assert name in str(e.value) and "CUDA tensor" in str(e.value)
