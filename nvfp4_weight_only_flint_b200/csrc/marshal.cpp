@@ -11,7 +11,8 @@
 // Every tensor is checked for what a kernel would read wrongly: it has to be a
 // contiguous CUDA tensor on the current device (whose stream the call takes)
 // of the element type the call takes and of at least the bytes it reads or
-// writes. A plain int passes as a device address.
+// writes. A plain int passes as a device address, but for the workspace, whose
+// size only a tensor tells.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -250,6 +251,10 @@ PyObject* paged_attention_call(PyObject* const* v) {
   void* ws = a.p(20, "workspace", Kind::kAny, 0, &ws_bytes);
   auto st = static_cast<int32_t*>(a.p(21, "status", Kind::kI32, 4));
   void* stream = a.stream(23);
+  if (!a.bad && PyLong_Check(v[20])) {
+    a.bad = true;
+    raise(FLINT_ERR_INVALID_ARG, "workspace: a tensor, for its size; the C call takes an address with its bytes");
+  }
   if (a.bad) return nullptr;
   return finish(flint_paged_attention(q, T, qs, kl, B, bt, mp, ps, np, k, vv, dt, ks, vs, hq, hkv, dh, max_q, window,
                                       scale, out, ws, static_cast<size_t>(ws_bytes), st, stream));

@@ -211,3 +211,13 @@ def test_bits_of_16_and_8_bit_types():
                 with pytest.raises(fm.FlintError) as e:
                     f(**{**only, name: args[name].view(dt)}, stream=0)
                 assert name in str(e.value) and "CUDA tensor" in str(e.value)
+
+
+def test_workspace_is_a_tensor():
+    # an address has no size: refused as such, not as too small
+    for e4m3 in (False, True):
+        import torch
+        args = {k: A if isinstance(v, torch.Tensor) else v for k, v in _paged_tensors(e4m3, True).items()}
+        with pytest.raises(fm.FlintError) as e:
+            fm.flint_paged_attention(**args, stream=0)
+        assert e.value.code == -1 and "workspace" in str(e.value) and "tensor" in str(e.value)
