@@ -498,7 +498,8 @@ int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32_t n_q_head
  * gives zeros (FLINT_DEVCHECK_INDEX); the keys and values of an invalid page
  * count as zero vectors. Keys and values inside a sequence's length have to be
  * finite: one that is not may reach every query of its sequence. Unwritten
- * rows and other sequences' rows may hold anything.
+ * rows and other sequences' rows may hold anything. A query head that holds a
+ * NaN gives NaN, in its own output alone.
  *   q, out    device bf16 [T][n_q_heads][128]; out must not overlap the inputs
  *   max_q_len host upper bound of n_s. max_q_len * (n_q_heads / n_kv_heads) <=
  *             16 takes the decode kernel (register-fragment tensor cores, keys

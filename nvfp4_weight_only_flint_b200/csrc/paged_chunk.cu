@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
       tc_fence_before();
       if (live) {
         if (im.slot < 0) {
-          const float f = (l > 0.f ? 1.f / l : 0.f) * (kE4M3 ? __ldg(p.v_scale + im.g) : 1.f);
+          const float f = (l == 0.f ? 0.f : 1.f / l) * (kE4M3 ? __ldg(p.v_scale + im.g) : 1.f);
           uint16_t* dst =
               p.out + (static_cast<size_t>(im.row0 + im.tok0 + tok) * p.Hq + im.g * p.group + row % p.group) * kDh;
           // out is 16-byte aligned: 32-byte stores where it is 32-byte aligned too
@@ -886,10 +886,11 @@ __global__ void __launch_bounds__(kCombineThreads) k_chunk_combine(PagedAttnPara
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // rows past the pair's tokens were not written: what is read for them is dropped below
-      if (!(ml[i].x > -INFINITY)) continue;
+      // rows past the pair's tokens were not written: what is read for them is dropped below. A piece without a
+      // maximum (-inf) adds zeros, or the NaN of a query.
       const float mx = fmaxf(M[i], ml[i].x);
-      const float f0 = M[i] == -INFINITY ? 0.f : exp2_ftz(M[i] - mx), f1 = exp2_ftz(ml[i].x - mx);
+      const float f0 = M[i] == -INFINITY ? 0.f : exp2_ftz(M[i] - mx);
+      const float f1 = ml[i].x == -INFINITY ? 0.f : exp2_ftz(ml[i].x - mx);
       M[i] = mx;
       l[i] = fmaf(l[i], f0, ml[i].y * f1);
       acc[i].x = fmaf(acc[i].x, f0, o[i].x * f1);
@@ -903,7 +904,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_chunk_combine(PagedAttnPara
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + i, rt = r % kTile, tok = sp.tok0 + (r / kTile) * tok_t + rt / p.group;
     if (rt >= tok_t * p.group || tok >= q.n) continue;
-    const float f = (l[i] > 0.f ? 1.f / l[i] : 0.f) * vs;
+    const float f = (l[i] == 0.f ? 0.f : 1.f / l[i]) * vs;
     const __nv_bfloat162 a = __floats2bfloat162_rn(acc[i].x * f, acc[i].y * f),
                          b = __floats2bfloat162_rn(acc[i].z * f, acc[i].w * f);
     reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(q.row0 + tok) * p.Hq + g * p.group + rt % p.group) * kDh)[lane] =

@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_decode(PagedAttnParams
       }
       if (whole) {
         const int tok = r / p.group, h = r - tok * p.group;
-        const __nv_bfloat16 bv = __float2bfloat16_rn(tot > 0.f ? acc / tot * vs : 0.f);
+        // a sum of 0: the row saw no key. NaN (from the query) stays.
+        const __nv_bfloat16 bv = __float2bfloat16_rn(tot == 0.f ? 0.f : acc / tot * vs);
         p.out[(static_cast<size_t>(ln.sq.row0 + tok) * p.Hq + g * p.group + h) * kDh + tid] =
             *reinterpret_cast<const uint16_t*>(&bv);
       } else {
@@ -597,7 +598,8 @@ struct Joined {
   float m, l;
   float4 o;
 };
-// Partials of row r in parts c0, c0 + step, ... up to i1; lane: four dimensions.
+// Partials of row r in parts c0, c0 + step, ... up to i1; lane: four dimensions. A partial without a maximum (-inf)
+// adds its sums times 0: zeros of a row that saw no key there, or the NaN of a query.
 template <int kStep>
 __device__ __forceinline__ Joined join_parts(const Ws& ws, int Hkv, int g, int c_first, int i1, int r, int lane) {
   Joined a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -618,7 +620,6 @@ __device__ __forceinline__ Joined join_parts(const Ws& ws, int Hkv, int g, int c
     float mb = a.m;
 #pragma unroll
     for (int i = 0; i < kCombineBatch; ++i) mb = fmaxf(mb, mlv[i].x);
-    if (mb == -INFINITY) continue;
     const float fo = a.m == -INFINITY ? 0.f : exp2_ftz(a.m - mb);
     a.l *= fo;
     a.o.x *= fo;
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) k_paged_combine(PagedAttnP
     for (int r = warp; r < ln.sq.n * p.group; r += kCombineWarps) {
       const Joined a = join_parts<1>(ws, p.Hkv, g, i0, i1, r, lane);
       const int tok = r / p.group, h = r - tok * p.group;
-      const float f = a.l > 0.f ? vs / a.l : 0.f;
+      const float f = a.l == 0.f ? 0.f : vs / a.l;
       reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(ln.sq.row0 + tok) * p.Hq + g * p.group + h) * kDh)[lane] =
           make_uint2(bf2(a.o.x * f, a.o.y * f), bf2(a.o.z * f, a.o.w * f));
     }
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) k_paged_combine(PagedAttnP
           den = fmaf(s_l[w], f, den);
           num = fmaf(s_acc[w][d], f, num);
         }
-        const __nv_bfloat16 bv = __float2bfloat16_rn(den > 0.f ? num / den * vs : 0.f);
+        const __nv_bfloat16 bv = __float2bfloat16_rn(den == 0.f ? 0.f : num / den * vs);
         p.out[(static_cast<size_t>(ln.sq.row0 + tok) * p.Hq + x) * kDh + d] = *reinterpret_cast<const uint16_t*>(&bv);
       }
       __syncthreads();

@@ -292,3 +292,27 @@ def test_chunk_is_the_same_in_every_run_and_graph():
     call(o2, w2, side)
     torch.cuda.synchronize()
     assert torch.equal(out, o2)
+
+
+# finished by one part, cut into parts and joined by row or by head; tile pairs whole, cut, dealt
+NAN_QUERY = [([1, 1, 1], [64, 65, 5000], 32, 4, 16), ([1] * 40, [3 + 100 * i for i in range(40)], 32, 4, 16),
+             ([2, 1], [9, 300], 32, 4, 16), ([1], [9000], 8, 1, 16), ([300, 5], [300, 77], 8, 1, 16),
+             ([40, 2], [20_000, 9000], 16, 2, 64), ([1500], [1500], 74, 74, 64)]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("case", range(len(NAN_QUERY)))
+def test_nan_in_a_query_stays_in_its_head(case, e4m3):
+    new, kv, hq, hkv, page = NAN_QUERY[case]
+    b = R.Paged(510 + case, new, kv, hq, hkv, page, e4m3)
+    hit = [(0, hq - 1), (b.rows // 2, 0), (b.rows - 1, hq // 2)]
+    clean = b.q.clone()
+    for t, h in hit:
+        b.q[t, h, 5] = float("nan")
+    got = R.run_attention(b)
+    b.q = clean
+    ref = R.attention(b)
+    for t, h in hit:
+        assert got[t, h].isnan().all(), (t, h)
+        got[t, h] = ref[t, h]
+    R.check_attention(got, b, what="the other heads")
