@@ -493,7 +493,8 @@ int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32_t n_q_head
  * token's position (window 0: every j <= pos), keys and values of kv head h /
  * (n_q_heads / n_kv_heads). fp32 scores, maxima and sums; the weights enter the
  * value sum rounded to bf16 (bf16 cache) or f16 (E4M3 cache, whose codes are
- * exact in f16; q then enters as f16 after an exact power-of-two scale per row).
+ * exact in f16; weights from 2^-25 of the largest on keep f16's 11 bits; q then
+ * enters as f16 after an exact power-of-two scale per row).
  * A sequence with an invalid kv_len, or with more than max_q_len new tokens,
  * gives zeros (FLINT_DEVCHECK_INDEX); the keys and values of an invalid page
  * count as zero vectors. Keys and values inside a sequence's length have to be

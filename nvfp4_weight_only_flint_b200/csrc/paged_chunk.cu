@@ -28,12 +28,14 @@
 //   O += P V      tcgen05.mma, P from tensor memory, V as it lies in the cache
 //                 (keys x dims: MN-major)
 // with the two tiles' softmax and MMAs alternating. O is rescaled only when a
-// row's maximum grew by more than 2^8 since the last time (P then stays below
-// 2^8; O / l is the same), by the softmax warps themselves, so no correction
-// warps stand in the chain. Tensor memory: S0 S1 O0 O1, 128 columns each.
+// row's maximum grew by more than kGrow since the last time (P then stays below
+// 2^kGrow; O / l is the same; a published form of the running softmax), by the
+// softmax warps themselves, so no correction warps stand in the chain. Tensor
+// memory: S0 S1 O0 O1, 128 columns each.
 //   bf16 cache: five 32 KB stages of K and V by TMA, one box per page (or 128 rows).
 //   E4M3 cache: three raw 16 KB stages; a further warpgroup turns them into f16
-//     tiles (exact), and Q into f16 after a power-of-two scale per row.
+//     tiles (exact), and Q into f16 after a power-of-two scale per row; P is f16
+//     times 2^kShift.
 // Keys past a sequence's end: S is masked by column, and V rows are zeroed in
 // shared memory, so whatever unused cache rows hold stays out of the sums.
 #include <cuda.h>
@@ -57,7 +59,6 @@ constexpr int kCtas = 148;
 constexpr int kFill = 2;                   // length of a tile pair on the line beyond its key tiles
 constexpr int kMinPart = 6;                // no part is shorter
 constexpr int kMaxSeqs = 32768;            // the scan over sequences lives in the stages' shared memory
-constexpr float kRescale = 8.f;            // log2 units
 
 template <bool kE4M3>
 struct Cfg {
@@ -65,6 +66,12 @@ struct Cfg {
   static constexpr int kStages = kE4M3 ? 3 : 5;
   static constexpr int kRaw = kE4M3 ? 3 : 0;
   static constexpr int kFullCount = kE4M3 ? 128 : 1;
+  // log2: a row's maximum may grow by 2^kGrow before O is rescaled, and P is 2^kShift times the weight, at most 2^(kGrow
+  // + kShift). f16 weights keep 11 bits from 2^-14 on, that is down to 2^-25 of the largest (growth by 2^8 and no shift,
+  // as for bf16: 2^-14 to 2^-22, and the keys behind a dominating one lost theirs). 1,024 tokens over 31,000, from a
+  // graph: 531 us, as with 2^8 unshifted (531 to 540); growth by 2^2 and a shift of 2^13 534 to 542.
+  static constexpr float kGrow = kE4M3 ? 4.f : 8.f;
+  static constexpr float kShift = kE4M3 ? 11.f : 0.f;
 };
 
 // A tile pair cut by part boundaries: its pieces are in parts first .. last.
@@ -402,6 +409,11 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
       }
       done_item(it);
       float m = -INFINITY, l = 0.f;
+      // what is subtracted from the scores; rounded up, no f16 weight passes 2^(kGrow + kShift)
+      auto base_of = [&](float mx) {
+        if (mx == -INFINITY) return 0.f;
+        return kE4M3 ? __fadd_ru(__fmul_ru(mx, c), -C::kShift) : mx * c;
+      };
       for (int kt = im.kt0; kt < im.kt1; ++kt) {
         if (!(ok = mma_wait(&ctl.s_full[t], cnt & 1, ab, status))) break;
         tc_fence_after();
@@ -428,13 +440,13 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
         if (kt == im.kt0) {
           m = mn;
         } else {
-          const bool grow = (mn - m) * c > kRescale || (m == -INFINITY && mn > m);
+          const bool grow = (mn - m) * c > C::kGrow || (m == -INFINITY && mn > m);
           if (__any_sync(0xffffffffu, grow)) {
             // P V of the previous tile has to be in O before O is rescaled
             if (!(ok = mma_wait(&ctl.o_done[t], (cnt - 1) & 1, ab, status))) break;
             tc_fence_after();
             const float mu = fmaxf(m, mn);
-            const float f = m == -INFINITY ? 0.f : exp2_ftz((m - mu) * c);
+            const float f = m == -INFINITY ? 0.f : exp2_ftz(base_of(m) - base_of(mu));
             m = mu;
             l *= f;
 #pragma unroll
@@ -448,8 +460,8 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
             }
           }
         }
-        const float mc = m == -INFINITY ? 0.f : m * c;
-        const f32x2 c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+        const float base = base_of(m);
+        const f32x2 c2 = pack2(c, c), mc2 = pack2(-base, -base);
         f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -517,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
           }
         } else {
           const size_t at = static_cast<size_t>(im.slot) * rows_per_slot + t * kTile + row;
-          *reinterpret_cast<float2*>(w.ml + at * 2) = make_float2(m == -INFINITY ? -INFINITY : m * c, l);
+          *reinterpret_cast<float2*>(w.ml + at * 2) = make_float2(m == -INFINITY ? -INFINITY : base_of(m), l);
           float* dst = w.po + at * kDh;  // 256-byte aligned in a workspace that is 32-byte aligned
           const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll

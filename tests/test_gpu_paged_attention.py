@@ -316,3 +316,35 @@ def test_nan_in_a_query_stays_in_its_head(case, e4m3):
         assert got[t, h].isnan().all(), (t, h)
         got[t, h] = ref[t, h]
     R.check_attention(got, b, what="the other heads")
+
+
+def _sink(seed, new, kv, hq, hkv, at):
+    """An E4M3 batch in which one key outweighs each other one 2^22 to 2^24.5 times and has a zero value, as attention
+    sinks do: the output is what the light keys leave. (The sink's key is along the queries, at a score of 16 nats =
+    23.1 bits; the others' scores have a deviation of 0.2 nats.)"""
+    b = R.Paged(seed, new, kv, hq, hkv, 16, e4m3=True)
+    g = torch.Generator().manual_seed(seed + 1)
+    base = torch.randn((hkv, R.DH), generator=g)
+    b.q = base.repeat_interleave(hq // hkv, 0) + 0.02 * torch.randn((b.T, hq, R.DH), generator=g)
+    b.q = b.q.to(torch.bfloat16)
+    k = torch.randn((b.n_pages, b.page, hkv, R.DH), generator=g) * 0.2
+    v = b.v.float()
+    for s in range(b.B):
+        p = at(kv[s])
+        page, row = int(b.table[s, p // b.page]), p % b.page
+        k[page, row] = base * (16.0 * R.DH ** 0.5 / base.square().sum(-1, keepdim=True))
+        v[page, row] = 0.0
+    k = (k / b.ks[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    v = v.to(torch.float8_e4m3fn).view(torch.uint8)
+    k[~b.live], v[~b.live] = 0x7F, 0x7F
+    b.k, b.v = k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn)
+    return b
+
+
+@pytest.mark.parametrize("new,kv", [([1, 1], [3000, 200]), ([2, 1], [700, 9000]), ([70, 9], [2000, 200]),
+                                    ([300], [700])])
+@pytest.mark.parametrize("at", ["first", "middle"])
+def test_light_keys_behind_a_heavy_one(new, kv, at):
+    # their weights have to keep f16's 11 bits (check_attention's bound), 2^-24.5 of the largest as they are
+    b = _sink(500, new, kv, 8, 2, (lambda n: 0) if at == "first" else (lambda n: n // 2))
+    R.check_attention(R.run_attention(b), b, what=f"{at} key")
