@@ -455,7 +455,7 @@ int flint_decode_attention(const uint16_t* q, const uint16_t* k_cache, const uin
  *   k_cache, v_cache  device pools [n_pages][page_size][n_kv_heads][128] of
  *             cache_dtype (flint_kv_dtype); page_size a power of two in
  *             16..1024, n_pages * page_size < 2^31.
- *   k_scale, v_scale  device fp32 [n_kv_heads], positive, for an E4M3 cache (a
+ *   k_scale, v_scale  device fp32 [n_kv_heads], positive and normal, for an E4M3 cache (a
  *             stored code stands for code * scale); ignored (NULL allowed) for bf16.
  *   status    nullable device int32: FLINT_DEVCHECK_INDEX is set by a page
  *             outside [0, n_pages), a kv_len[s] below n_s or above max_pages *

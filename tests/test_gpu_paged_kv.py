@@ -123,6 +123,20 @@ def test_append_saturates_e4m3_and_large_values():
     assert float(got[1].float().abs().nan_to_num(0).max()) == 448.0
 
 
+@pytest.mark.parametrize("scale", [1.0, 3 / 128, 0.05, 7 / 64, 0.3])
+def test_append_e4m3_codes_of_halfway_values(scale):
+    # bf16 values over every binade that has codes, many halfway between two: the code is that of the fp32 quotient
+    b = R.Paged(3, [16], [16], 4, 4, 16, e4m3=True)
+    x = torch.arange(0x3800, 0x3800 + 16 * 4 * R.DH).to(torch.int16).view(torch.bfloat16).view(16, 4, R.DH)
+    b.qkv[:, 4:8], b.qkv[:, 8:] = x, -x
+    b.ks, b.vs = torch.full((4,), scale), torch.full((4,), scale)
+    _, k, v = _run(b, None, None, None, False)
+    want = (x.float() / torch.tensor(scale)).clamp(-448, 448)
+    page = int(b.table[0, 0])
+    assert torch.equal(k[page].view(torch.uint8), want.to(torch.float8_e4m3fn).view(torch.uint8))
+    assert torch.equal(v[page].view(torch.uint8), (-want).to(torch.float8_e4m3fn).view(torch.uint8))
+
+
 def test_append_skips_what_has_no_place():
     b = R.Paged(8, [2, 3, 4, 1], [20, 40, 10, 33], 6, 2, 16, pad=1)
     b.table[1, 2] = b.n_pages          # positions 37..39 of sequence 1 have no page
