@@ -537,7 +537,8 @@ int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t* q_start, 
  * vocabulary order, whose running sum of kept w exceeds u times the kept total;
  * its log-probability is ln(w / kept total). Masses are summed as integers of
  * 2^-45 of the largest (at 2^18 tokens; finer below, coarser above): the result
- * is the same in every run, and a token below half of that is never drawn.
+ * is the same in every run, and a token below half of that is never drawn. The
+ * log-probability is of the token's own logit, not of its mass so rounded.
  *   status      nullable device int32. A row without any logit above -inf sets
  *               FLINT_DEVCHECK_NONFINITE, one with a negative or NaN temperature
  *               or u outside [0, 1) FLINT_DEVCHECK_INDEX; both give token -1,

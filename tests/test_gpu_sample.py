@@ -248,3 +248,17 @@ def test_sample_refuses_tensors_it_would_read_wrongly():
         with pytest.raises(fm.FlintError) as e:
             call(**bad)
         assert e.value.code == -1
+
+
+@pytest.mark.parametrize("V", [1000, 20_001, 150_144, 400_000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sample_log_probability_of_a_light_token(V, dtype):
+    # u = 0 draws the first token, of a few units of mass only; every form of the draw (ranks counted, sorted, whole row)
+    x = torch.full((7, V), -math.inf)
+    x[:, 0] = torch.tensor([-29.0, -30.0, -29.5, -28.7, -25.0, -20.0, -29.25])
+    x[:, V // 2:V // 2 + 40] = torch.linspace(-1, 0, 40)
+    x[2, V // 4:V // 4 + 200] = torch.linspace(-3, -2, 200)
+    x[3, V // 4:V // 4 + 240] = torch.linspace(-3, -2, 240)
+    x[5, :V // 8] = -20.0
+    x[6] = x[6].clamp_min(-29.25)
+    _check(x.to(dtype), [1.0] * 7, [0, 60, 500, 300, 700, 0, 0], [1.0] * 7, [0.0] * 7, [0.0] * 7)
