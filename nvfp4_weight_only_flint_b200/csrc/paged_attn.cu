@@ -51,7 +51,8 @@ extern "C" int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t
   p.Hq = n_q_heads;
   p.Hkv = n_kv_heads;
   p.group = n_q_heads / n_kv_heads;
-  p.window = window;
+  // a window no shorter than the longest sequence is none: positions minus the window stay within int
+  p.window = window < kPagedMaxPos ? window : 0;
   p.max_q = max_q_len < T ? max_q_len : T;  // as for the workspace size
   p.scale = scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -348,3 +348,15 @@ def test_light_keys_behind_a_heavy_one(new, kv, at):
     # their weights have to keep f16's 11 bits (check_attention's bound), 2^-24.5 of the largest as they are
     b = _sink(500, new, kv, 8, 2, (lambda n: 0) if at == "first" else (lambda n: n // 2))
     R.check_attention(R.run_attention(b), b, what=f"{at} key")
+
+
+@pytest.mark.parametrize("new,kv", [([1, 2], [700, 90]), ([150, 1, 20], [150, 700, 333])])
+def test_windows_past_every_position(new, kv):
+    # up to the largest int: the same as no window, bit for bit
+    for e4m3 in (False, True):
+        b = R.Paged(530, new, kv, 8, 2, 16, e4m3)
+        whole = R.run_attention(b)
+        R.check_attention(whole, b)
+        for window in (2 ** 30, 2 ** 31 - 1):
+            assert torch.equal(R.run_attention(b, window), whole)
+        R.check_attention(R.run_attention(b, 2 ** 30 - 1), b)
