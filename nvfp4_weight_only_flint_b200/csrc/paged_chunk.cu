@@ -93,7 +93,8 @@ __host__ __device__ inline size_t carve(Ws* w, char* ws, int Hkv, int rows) {
   char* p = ws;
   w->flags = reinterpret_cast<int*>(p);
   p += 256;
-  const size_t parts = parts_per_head(Hkv), slots = parts * Hkv * 2;
+  // a kv head of one part cuts no pair
+  const size_t parts = parts_per_head(Hkv), slots = parts > 1 ? parts * Hkv * 2 : 0;
   w->splits = reinterpret_cast<Split*>(p);
   p += up256(parts * sizeof(Split));
   w->ml = reinterpret_cast<float*>(p);

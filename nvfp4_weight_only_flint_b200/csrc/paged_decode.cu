@@ -160,9 +160,14 @@ struct Ws {
 };
 __host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 __host__ __device__ inline int ctas_per_head(int Hkv) { return Hkv >= kCtaSlots ? 1 : kCtaSlots / Hkv; }
+// Partials; a kv head of one CTA cuts no sequence.
+__host__ __device__ inline size_t slots_of(int Hkv) {
+  const int g = ctas_per_head(Hkv);
+  return g > 1 ? static_cast<size_t>(g) * Hkv * 2 : 0;
+}
 __host__ __device__ inline Ws carve(char* ws, int B, int Hkv) {
   Ws w;
-  const size_t slots = static_cast<size_t>(ctas_per_head(Hkv)) * Hkv * 2;
+  const size_t slots = slots_of(Hkv);
   w.pre = reinterpret_cast<long long*>(ws);
   ws += up256((static_cast<size_t>(B) + 1) * sizeof(long long));
   w.ml = reinterpret_cast<float*>(ws);
@@ -724,8 +729,7 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
 
 size_t paged_decode_workspace(int B, int n_kv_heads) {
   const Ws w = carve(nullptr, B, n_kv_heads);
-  const size_t slots = static_cast<size_t>(ctas_per_head(n_kv_heads)) * n_kv_heads * 2;
-  return reinterpret_cast<size_t>(w.po) + slots * kRowsMax * kDh * sizeof(float);
+  return reinterpret_cast<size_t>(w.po) + slots_of(n_kv_heads) * kRowsMax * kDh * sizeof(float);
 }
 
 int paged_decode_launch(const PagedAttnParams& p, int cache_dtype, size_t ws_bytes, cudaStream_t st) {

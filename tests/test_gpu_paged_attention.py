@@ -360,3 +360,17 @@ def test_windows_past_every_position(new, kv):
         for window in (2 ** 30, 2 ** 31 - 1):
             assert torch.equal(R.run_attention(b, window), whole)
         R.check_attention(R.run_attention(b, 2 ** 30 - 1), b)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hkv", [75, 148, 297])
+def test_one_part_a_kv_head(hkv, e4m3):
+    # nothing is cut, and the workspace holds no partials
+    for new, kv in (([1, 2, 0], [900, 70, 3]), ([40, 3], [300, 150])):
+        b = R.Paged(hkv, new, kv, hkv, hkv, 16, e4m3)
+        nb = fm.flint_paged_attention_workspace_bytes(b.T, b.B, hkv, hkv, max(new))
+        if hkv >= 148 and max(new) > 16 or hkv > 148:
+            assert nb < 1e5
+        behind = torch.full((nb + 4096,), 0x55, dtype=torch.uint8, device="cuda")
+        R.check_attention(R.run_attention(b, ws=behind), b, what=f"{hkv} kv heads")
+        assert (behind[nb:] == 0x55).all()

@@ -221,3 +221,12 @@ def test_workspace_is_a_tensor():
         with pytest.raises(fm.FlintError) as e:
             fm.flint_paged_attention(**args, stream=0)
         assert e.value.code == -1 and "workspace" in str(e.value) and "tensor" in str(e.value)
+
+
+def test_attention_workspace_is_bounded(L):
+    # partials are kept only where a kv head's work is cut: 39 MB at most for prompt pieces, 5 MB and the prefix sums for
+    # decode steps, whatever the number of kv heads
+    for hkv in list(range(1, 160)) + [296, 297, 512, 1024]:
+        assert 0 < fm.flint_paged_attention_workspace_bytes(4096, 1, hkv, hkv, 4096) < 39.5e6, hkv
+        assert 0 < fm.flint_paged_attention_workspace_bytes(64, 64, hkv, hkv, 1) < 5.2e6, hkv
+    assert fm.flint_paged_attention_workspace_bytes(4096, 1, 1024, 1024, 4096) < 1e5
