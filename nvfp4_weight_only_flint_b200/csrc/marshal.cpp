@@ -154,7 +154,19 @@ int device_now() {
   }
 }
 
-PyObject* finish(int rc) {
+// Makes the C call without the interpreter lock: a launch waits where the stream's queue is full, and other threads (a
+// host function that the stream waits for, even) go on meanwhile. The caller holds the tensors.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F>
+PyObject* launch(F call) {
+  int rc;
+  {
+    const Unlocked u;
+    rc = call();
+  }
   if (rc != FLINT_OK) {
     raise(rc, flint_last_error());
     return nullptr;
@@ -221,8 +233,10 @@ PyObject* paged_kv_call(PyObject* const* v) {
   auto st = static_cast<int32_t*>(a.p(23, "status", Kind::kI32, 4));
   void* stream = a.stream(25);
   if (a.bad) return nullptr;
-  return finish(flint_qk_norm_rope_paged_kv(qkv, T, hq, hkv, dh, qw, kw, cs, max_pos, rope, eps, qs, kl, B, bt, mp, ps,
-                                            np, dt, ks, vs, q_out, k, vv, st, stream));
+  return launch([&] {
+    return flint_qk_norm_rope_paged_kv(qkv, T, hq, hkv, dh, qw, kw, cs, max_pos, rope, eps, qs, kl, B, bt, mp, ps, np,
+                                       dt, ks, vs, q_out, k, vv, st, stream);
+  });
 }
 
 // q T | q_start kv_len B table max_pages page n_pages | k v dtype ks vs | Hq Hkv max_q window scale out ws status
@@ -256,8 +270,10 @@ PyObject* paged_attention_call(PyObject* const* v) {
     raise(FLINT_ERR_INVALID_ARG, "workspace: a tensor, for its size; the C call takes an address with its bytes");
   }
   if (a.bad) return nullptr;
-  return finish(flint_paged_attention(q, T, qs, kl, B, bt, mp, ps, np, k, vv, dt, ks, vs, hq, hkv, dh, max_q, window,
-                                      scale, out, ws, static_cast<size_t>(ws_bytes), st, stream));
+  return launch([&] {
+    return flint_paged_attention(q, T, qs, kl, B, bt, mp, ps, np, k, vv, dt, ks, vs, hq, hkv, dh, max_q, window,
+                                 scale, out, ws, static_cast<size_t>(ws_bytes), st, stream);
+  });
 }
 
 // logits rows vocab row_stride dtype temperature top_k top_p min_p u tokens logprobs status stream
@@ -277,7 +293,9 @@ PyObject* sample_call(PyObject* const* v) {
   auto st = static_cast<int32_t*>(a.p(12, "status", Kind::kI32, 4));
   void* stream = a.stream(13);
   if (a.bad) return nullptr;
-  return finish(flint_sample(x, rows, vocab, stride, dt, t, k, p, m, u, tok, lp, st, stream));
+  return launch([&] {
+    return flint_sample(x, rows, vocab, stride, dt, t, k, p, m, u, tok, lp, st, stream);
+  });
 }
 
 PyObject* paged_kv(PyObject* m, PyObject* const* v, Py_ssize_t n) { return guarded<paged_kv_call>(m, v, n, 26); }

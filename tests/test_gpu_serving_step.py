@@ -130,3 +130,35 @@ def test_serving_steps(e4m3):
         params[3].copy_(torch.rand(B, generator=g).cuda())
         graph.replay()
         _check(s, b, qkv, [1] * B, kv, keep, params)
+
+
+def test_other_threads_run_while_a_launch_waits():
+    """A launch into a full queue waits for the GPU, without the interpreter lock."""
+    import threading
+    import time
+    x, u = torch.zeros((1, 100), device="cuda"), torch.zeros(1, device="cuda")
+    tok = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = lambda: fm.flint_sample(x, 1, 100, 100, fm.FLINT_LOGITS_F32, None, None, None, None, u, tok)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    gap, stop = [0.0], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gap[0], last = max(gap[0], now - last), now
+
+    other = threading.Thread(target=tick)
+    other.start()
+    torch.cuda._sleep(1_000_000_000)  # half a second: more launches behind it than the queue holds
+    longest = 0.0
+    for _ in range(3000):
+        t = time.perf_counter()
+        call()
+        longest = max(longest, time.perf_counter() - t)
+    stop.set()
+    other.join()
+    torch.cuda.synchronize()
+    assert longest < 0.1 or gap[0] < longest / 2, (longest, gap[0])
