@@ -13,6 +13,7 @@ SO = os.path.join(PKG, "libflint_moe.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 OBJ_DIR = os.path.join(PKG, "_build")
+MARSHAL_FOR = os.path.join(OBJ_DIR, "marshal.txt")  # what _marshal.so was built for
 # translation units, compiled in parallel and linked into one shared library
 SOURCES = ["flint_moe.cu", "tok1.cu", "tokn.cu", "lmhead.cu", "attn.cu", "attn_decode.cu", "ep.cu",
            "paged_kv.cu", "paged_attn.cu", "paged_decode.cu", "paged_chunk.cu", "sample.cu"]
@@ -26,11 +27,25 @@ def _inputs():
     return files
 
 
+def _marshal_built_for() -> str:
+    """The interpreter and the torch that the extension module is compiled for (read without importing torch)."""
+    from importlib.metadata import version
+    return f"python {sys.version} torch {version('torch')}"
+
+
+def _marshal_is_current() -> bool:
+    header = os.path.join(INCLUDE, "flint_moe.h")
+    if not os.path.exists(MARSHAL) or not os.path.exists(MARSHAL_FOR):
+        return False
+    with open(MARSHAL_FOR) as f:
+        if f.read() != _marshal_built_for():
+            return False
+    return all(os.path.getmtime(f) <= os.path.getmtime(MARSHAL) for f in (MARSHAL_SRC, header))
+
+
 def _build_marshal(force: bool, verbose: bool) -> None:
     """The extension module needs torch's headers and links against torch and libflint_moe.so (found beside it)."""
-    header = os.path.join(INCLUDE, "flint_moe.h")
-    if not force and os.path.exists(MARSHAL) and all(
-            os.path.getmtime(f) <= os.path.getmtime(MARSHAL) for f in (MARSHAL_SRC, header)):
+    if not force and _marshal_is_current():
         return
     import sysconfig
 
@@ -47,6 +62,9 @@ def _build_marshal(force: bool, verbose: bool) -> None:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, MARSHAL)
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with open(MARSHAL_FOR, "w") as f:
+        f.write(_marshal_built_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
