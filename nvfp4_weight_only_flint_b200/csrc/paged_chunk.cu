@@ -18,8 +18,7 @@
 // against 503, since 128 items do not fill 148 CTAs, and a mixed step 66 us
 // against 60, 10 of them the list.) Where pairs are many and short beside a part
 // (deal_whole), they are dealt out whole instead, from the last one of the line
-// (a prompt's longest) and back and forth: a prompt of 8,192 tokens 512 us
-// against 550, without partials.
+// (a prompt's longest) and back and forth, without partials.
 //
 // Per key tile and query tile
 //   S = Q K^T     tcgen05.mma, both operands in shared memory (TMA, 128-byte swizzle)
@@ -166,9 +165,16 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s_warp, 
 }
 
 // Whole pairs, dealt back and forth: four or more a CTA, none longer than a
-// third of a part.
+// third of a part; that is even for one sequence, whose pairs grow steadily, and
+// for several if no pair is longer than 1.6 times the mean. Dealt / cut, us (in
+// brackets the longest pair over the mean): a prompt of 8,192 502 to 517 / 522 to
+// 528, 16 prompts of 512 [1.3] 85 / 91, 8 of 1,024 [1.5] 114 to 117 / 119 to 123,
+// 64 pieces of 128 over up to 1,000 keys [1.7] 136 / 129, 5 prompts of 1,500 to
+// 1,777 [1.7] 165 / 152 to 166, 32 pieces of 256 over up to 2,000 [1.9] 218 / 191,
+// 16 of 512 over up to 4,000 [2.3] 352 / 256.
 __device__ __forceinline__ bool deal_whole(int B, long long n_pairs, int longest, long long total, int n_parts) {
-  return B <= kDealSeqs && n_pairs >= 4ll * n_parts && 3ll * longest * n_parts <= total;
+  return B <= kDealSeqs && n_pairs >= 4ll * n_parts && 3ll * longest * n_parts <= total &&
+         (B == 1 || 5ll * longest * n_pairs <= 8 * total);
 }
 
 // All threads of the CTA. first_pair: scratch for B + 1 ints. Parts: place i of

@@ -374,3 +374,13 @@ def test_one_part_a_kv_head(hkv, e4m3):
         behind = torch.full((nb + 4096,), 0x55, dtype=torch.uint8, device="cuda")
         R.check_attention(R.run_attention(b, ws=behind), b, what=f"{hkv} kv heads")
         assert (behind[nb:] == 0x55).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("new,kv", [([384] * 4, [1084, 384, 1084, 384]), ([128] * 12, [228] * 12),
+                                    ([100] * 10, [1600, 100, 100, 1600, 1600, 100, 100, 1600, 1600, 100])])
+def test_chunk_pairs_dealt_or_cut(new, kv, e4m3):
+    # two CTAs a kv head, ten or twelve tile pairs: dealt whole in the first two batches, cut in the last, whose long
+    # pairs would all go to one CTA
+    b = R.Paged(540 + len(new), new, kv, 148, 74, 64, e4m3)
+    R.check_attention(R.run_attention(b), b, what=str((new[:4], kv[:4])))
