@@ -384,3 +384,29 @@ def test_chunk_pairs_dealt_or_cut(new, kv, e4m3):
     # pairs would all go to one CTA
     b = R.Paged(540 + len(new), new, kv, 148, 74, 64, e4m3)
     R.check_attention(R.run_attention(b), b, what=str((new[:4], kv[:4])))
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_steps_without_any_token_write_nothing(max_q):
+    for e4m3 in (False, True):
+        b = R.Paged(550, [0, 0, 0], [5, 900, 0], 8, 2, 16, e4m3, pad=3)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for start in ([0, 0, 0, 0], [2, 2, 2, 2], [3, 3, 3, 3]):
+            b.q_start = torch.tensor(start, dtype=torch.int32)
+            assert R.run_attention(b, max_q=max_q, status=st).isnan().all()
+        assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_unsorted_q_start_stays_within_the_call(e4m3):
+    # sequences that begin behind their ends, or share rows, are flagged or race for their rows; nothing else is touched
+    for max_q in (2, 40):
+        b = R.Paged(560, [2, 2, 2], [60, 60, 60], 8, 2, 16, e4m3, pad=4)
+        for start in ([4, 6, 0, 2], [6, 0, 2, 1], [0, 2, -5, 2], [2, 2 ** 31 - 1, 0, 2], [-2 ** 31, 0, 1, 2]):
+            b.q_start = torch.tensor(start, dtype=torch.int32)
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            out = R.run_attention(b, max_q=max_q, status=st)
+            assert int(st.item()) == fm.FLINT_DEVCHECK_INDEX
+            owned = {t for x, y in zip(start, start[1:]) if 0 <= x <= y <= b.T for t in range(x, y)}
+            for t in range(b.T):
+                assert out[t].isnan().all() == (t not in owned), (start, t)
