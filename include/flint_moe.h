@@ -471,7 +471,7 @@ int flint_decode_attention(const uint16_t* q, const uint16_t* k_cache, const uin
  *   qkv      device bf16 [T][n_q_heads + 2*n_kv_heads][128]
  *   q_norm_w, k_norm_w  device bf16 [128], or both NULL: no normalisation
  *   cos_sin, max_pos, rope  as there; the row is the token's position
- *   q_out    device bf16 [T][n_q_heads][128]
+ *   q_out    device bf16 [T][n_q_heads][128]; must not overlap qkv
  * One rounding, from fp32: to bf16, or for an E4M3 cache of y / scale to the
  * nearest code, saturating at +-448. A token without a valid page keeps its
  * key and value unwritten, one whose position is at or past max_pos its
@@ -495,6 +495,8 @@ int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32_t n_q_head
  * value sum rounded to bf16 (bf16 cache) or f16 (E4M3 cache, whose codes are
  * exact in f16; weights from 2^-25 of the largest on keep f16's 11 bits; q then
  * enters as f16 after an exact power-of-two scale per row).
+ * The sum is divided by that of the weights, as rounded in the decode kernel, in
+ * fp32 in the chunk kernel.
  * A sequence with an invalid kv_len, or with more than max_q_len new tokens,
  * gives zeros (FLINT_DEVCHECK_INDEX); the keys and values of an invalid page
  * count as zero vectors. Keys and values inside a sequence's length have to be
@@ -504,12 +506,15 @@ int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32_t n_q_head
  *   q, out    device bf16 [T][n_q_heads][128]; out must not overlap the inputs
  *   max_q_len host upper bound of n_s. max_q_len * (n_q_heads / n_kv_heads) <=
  *             16 takes the decode kernel (register-fragment tensor cores, keys
- *             split evenly over the GPU), more the chunk kernel (tcgen05).
+ *             split evenly over the GPU), more the chunk kernel (tcgen05), whose
+ *             status also has FLINT_DEVCHECK_WAIT if a wait in it gave up (its
+ *             outputs are undefined then).
  *   workspace flint_paged_attention_workspace_bytes(T, B, n_q_heads, n_kv_heads,
  *             max_q_len) bytes, 16-byte aligned, overwritten by every call; calls
  *             that may run at the same time need one each.
  * n_q_heads / n_kv_heads an integer <= 16, n_q_heads <= 1024, B <= 32768,
- * T <= 2^24, max_q_len and n_pages >= 1, window >= 0, scale finite and > 0. Asynchronous on `stream`. */
+ * T <= 2^24, max_q_len and n_pages >= 1, window >= 0, scale finite and > 0.
+ * Asynchronous on `stream`. */
 size_t flint_paged_attention_workspace_bytes(int32_t T, int32_t B, int32_t n_q_heads, int32_t n_kv_heads,
                                              int32_t max_q_len);
 int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t* q_start, const int32_t* kv_len, int32_t B,

@@ -44,7 +44,10 @@ int paged_chunk_launch(const PagedAttnParams& p, int cache_dtype, size_t ws_byte
 size_t paged_chunk_workspace(int n_q_heads, int n_kv_heads, int max_q);
 
 // New tokens times query heads per kv head that one 16-row register tile
-// holds: such calls take the decode kernel, others the chunk kernel.
+// holds: such calls take the decode kernel, others the chunk kernel with its
+// 128-row tiles. Two tokens of a group of 8 (16 rows), decode / chunk kernel, us:
+// 1 x 4,098 keys 13.5 / 23.9, 64 x 4,098 107 / 126, 8 x 32,002 102 / 118, in E4M3
+// 13.0 / 27.1, 74.8 / 142, 72.1 / 130.
 constexpr int kDecodeRows = 16;
 
 }  // namespace flint

@@ -19,6 +19,8 @@
 // against 60, 10 of them the list.) Where pairs are many and short beside a part
 // (deal_whole), they are dealt out whole instead, from the last one of the line
 // (a prompt's longest) and back and forth, without partials.
+// Times here are of calls replayed from a graph; one by one they take up to 10 %
+// longer.
 //
 // Per key tile and query tile
 //   S = Q K^T     tcgen05.mma, both operands in shared memory (TMA, 128-byte swizzle)
@@ -56,7 +58,9 @@ constexpr int kHalfBytes = kTileBytes / 2; // 64 dims of a tile
 constexpr int kRawBytes = kTile * kDh;
 constexpr int kCtas = 148;
 constexpr int kFill = 2;                   // length of a tile pair on the line beyond its key tiles
-constexpr int kMinPart = 6;                // no part is shorter
+constexpr int kMinPart = 6;                // a line has at most total / kMinPart parts, rounded up
+// So no part is shorter than kMinPart / 2, and each reaches past a pair's first kFill places.
+static_assert(kMinPart / 2 > kFill, "a part within a pair's first kFill places would leave no partial, but be joined");
 constexpr int kMaxSeqs = 32768;            // the scan over sequences lives in the stages' shared memory
 
 template <bool kE4M3>
@@ -65,10 +69,10 @@ struct Cfg {
   static constexpr int kStages = kE4M3 ? 3 : 5;
   static constexpr int kRaw = kE4M3 ? 3 : 0;
   static constexpr int kFullCount = kE4M3 ? 128 : 1;
-  // log2: a row's maximum may grow by 2^kGrow before O is rescaled, and P is 2^kShift times the weight, at most 2^(kGrow
-  // + kShift). f16 weights keep 11 bits from 2^-14 on, that is down to 2^-25 of the largest (growth by 2^8 and no shift,
-  // as for bf16: 2^-14 to 2^-22, and the keys behind a dominating one lost theirs). 1,024 tokens over 31,000, from a
-  // graph: 531 us, as with 2^8 unshifted (531 to 540); growth by 2^2 and a shift of 2^13 534 to 542.
+  // log2: a row's maximum may grow by 2^kGrow before O is rescaled, and P is 2^kShift times the weight, at most
+  // 2^(kGrow + kShift). f16 weights keep 11 bits from 2^-14 on, that is down to 2^-25 of the largest (growth by 2^8 and
+  // no shift, as for bf16: 2^-14 to 2^-22, and the keys behind a dominating one lost theirs). 1,024 tokens over 31,000:
+  // 531 us, as with 2^8 unshifted (531 to 540); growth by 2^2 and a shift of 2^13 534 to 542.
   static constexpr float kGrow = kE4M3 ? 4.f : 8.f;
   static constexpr float kShift = kE4M3 ? 11.f : 0.f;
 };
@@ -177,8 +181,8 @@ __device__ __forceinline__ bool deal_whole(int B, long long n_pairs, int longest
          (B == 1 || 5ll * longest * n_pairs <= 8 * total);
 }
 
-// All threads of the CTA. first_pair: scratch for B + 1 ints. Parts: place i of
-// n is total i / n; n is chosen here so that no part is shorter than kMinPart.
+// All threads of the CTA. first_pair: scratch for B ints. Parts: place i of n is
+// total i / n; n is chosen here, at most total / kMinPart (rounded up).
 template <int kThreads>
 __device__ __forceinline__ void find_start(const PagedAttnParams& p, int part, int* n_parts, int* first_pair,
                                            long long* s_warp, Start* start) {
@@ -469,6 +473,8 @@ __global__ void __launch_bounds__(Cfg<kE4M3>::kThreads, 1)
         }
         const float base = base_of(m);
         const f32x2 c2 = pack2(c, c), mc2 = pack2(-base, -base);
+        // The sum is of the fp32 weights; adding them as rounded, as the decode kernel does, would take two more
+        // instructions a pair. Either is within the weights' rounding.
         f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
