@@ -511,7 +511,8 @@ int flint_qk_norm_rope_paged_kv(const uint16_t* qkv, int32_t T, int32_t n_q_head
  *             outputs are undefined then).
  *   workspace flint_paged_attention_workspace_bytes(T, B, n_q_heads, n_kv_heads,
  *             max_q_len) bytes, 16-byte aligned, overwritten by every call; calls
- *             that may run at the same time need one each.
+ *             that may run at the same time need one each. Enough for every call
+ *             with the same heads and no larger T, B and max_q_len.
  * n_q_heads / n_kv_heads an integer <= 16, n_q_heads <= 1024, B <= 32768,
  * T <= 2^24, max_q_len and n_pages >= 1, window >= 0, scale finite and > 0.
  * Asynchronous on `stream`. */

@@ -10,9 +10,11 @@ extern "C" size_t flint_paged_attention_workspace_bytes(int32_t T, int32_t B, in
   const int group = n_q_heads / n_kv_heads;
   if (group > kDecodeRows || B > 32768 || n_q_heads > 1024 || T > (1 << 24)) return 0;
   if (max_q_len > T) max_q_len = T;
-  return static_cast<long long>(max_q_len) * group <= kDecodeRows
-             ? paged_decode_workspace(B, n_kv_heads)
-             : paged_chunk_workspace(n_q_heads, n_kv_heads, max_q_len);
+  // never less than a smaller call takes: one workspace serves the decode steps beside the prompt pieces
+  const size_t decode = paged_decode_workspace(B, n_kv_heads);
+  if (static_cast<long long>(max_q_len) * group <= kDecodeRows) return decode;
+  const size_t chunk = paged_chunk_workspace(n_q_heads, n_kv_heads, max_q_len);
+  return chunk > decode ? chunk : decode;
 }
 
 extern "C" int flint_paged_attention(const uint16_t* q, int32_t T, const int32_t* q_start, const int32_t* kv_len,

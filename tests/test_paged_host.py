@@ -230,3 +230,18 @@ def test_attention_workspace_is_bounded(L):
         assert 0 < fm.flint_paged_attention_workspace_bytes(4096, 1, hkv, hkv, 4096) < 39.5e6, hkv
         assert 0 < fm.flint_paged_attention_workspace_bytes(64, 64, hkv, hkv, 1) < 5.2e6, hkv
     assert fm.flint_paged_attention_workspace_bytes(4096, 1, 1024, 1024, 4096) < 1e5
+
+
+def test_attention_workspace_serves_smaller_calls(L):
+    # sized once for the largest step, as the README has it
+    sizes = ((1, 1, 1), (2, 1, 2), (16, 4, 16), (64, 64, 1), (64, 5, 17), (300, 64, 200), (4096, 3000, 1),
+             (4096, 32768, 4096), (1 << 24, 32768, 1 << 24))
+    for hkv in (1, 4, 37, 74, 75, 100, 148, 149, 297, 1024):
+        for group in (1, 8):
+            if hkv * group > 1024:
+                continue
+            need = {x: fm.flint_paged_attention_workspace_bytes(x[0], x[1], hkv * group, hkv, x[2]) for x in sizes}
+            for x, nx in need.items():
+                for y, ny in need.items():
+                    if all(a <= b for a, b in zip(x, y)):
+                        assert nx <= ny, (hkv, group, x, y)
